@@ -1,0 +1,142 @@
+"""tp_linear_colwise_fp8 and tp_linear_rowwise_fp8 against the definition in 64 bits on the same
+codes and scales, and exactly on operands whose sums fp32 holds."""
+import pytest
+import torch
+
+import block_reference as ref
+import tensor_sharded_linear_amd as tsl
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _pair(values_u8_codes, scale_bytes):
+    """Device (codes, scales) with scale rows padded to whole dwords, the padding filled with NaN bytes."""
+    m, kb = scale_bytes.shape
+    s = torch.full((m, -(-kb // 4) * 4), 255, dtype=torch.uint8)
+    s[:, :kb] = scale_bytes
+    return values_u8_codes.cuda(), s.cuda().view(torch.float8_e8m0fnu)[:, :kb]
+
+
+def _integers(g, rows, k):
+    c = torch.randint(-4, 5, (rows, k), generator=g).float().to(torch.float8_e4m3fn)
+    return _pair(c, torch.randint(127, 129, (rows, k // 128), generator=g, dtype=torch.uint8))
+
+
+def _normal(g, rows, k, scale=1.0):
+    return tsl.tp_quantize_fp8((torch.randn(rows, k, generator=g) * scale * torch.exp(torch.randn(1, k, generator=g) / 2)).cuda())
+
+
+ROWS = [1, 2, 3, 5, 8, 15, 16, 17, 31, 33, 48, 63, 64, 65, 80, 97, 112, 127, 128, 129, 192, 193, 224, 255, 256, 257, 400]
+
+
+@pytest.mark.parametrize("m", ROWS)
+@pytest.mark.parametrize("n,k", [(16, 128), (48, 640), (144, 1152), (272, 384), (528, 256)])
+def test_exact_on_small_integers(m, n, k):
+    """Codes -4..4 and scales 1 or 2: every partial sum is an integer below 2^24, so any order of
+    fp32 additions gives the exact sum.  Every row, column and scale has its own value, so a
+    misplaced one shows."""
+    g = torch.Generator().manual_seed(m * 7919 + n * 31 + k)
+    x, w = _integers(g, m, k), _integers(g, n, k)
+    y = tsl.tp_linear_rowwise_fp8(*x, *w)
+    want = ref.values(*x) @ ref.values(*w).t()
+    assert torch.equal(y.cpu().double(), want)
+
+
+@pytest.mark.parametrize("m", [1, 4, 16, 23, 64, 77, 128, 130, 333])
+@pytest.mark.parametrize("act,bias,out", [("none", False, BF), ("none", True, F32), ("gelu_tanh", True, BF),
+                                          ("gelu_tanh", False, F32), ("swiglu", True, BF), ("swiglu", False, F32)])
+def test_epilogues_within_the_derived_bound(m, act, bias, out):
+    n, k = 208, 896
+    g = torch.Generator().manual_seed(m)
+    rows = 2 * n if act == "swiglu" else n
+    x, w = _normal(g, m, k), _normal(g, rows, k, k ** -0.5)
+    b = torch.randn(rows, generator=g).to(BF).cuda() if bias else None
+    y = tsl.tp_linear_colwise_fp8(*x, *w, b, act=act, out_dtype=out)
+    assert y.dtype == out
+    ref.check(y, *ref.linear(ref.values(*x), ref.values(*w), b, act), what=f"{m} {act}")
+
+
+@pytest.mark.parametrize("m,n,k", [(700, 1040, 2304), (1500, 2320, 768), (4608, 272, 128), (90, 4624, 512),
+                                   (1, 9232, 6144), (2, 16, 18432)])
+def test_many_tiles(m, n, k):
+    g = torch.Generator().manual_seed(m + n + k)
+    x, w = _integers(g, m, k), _integers(g, n, k)
+    y = tsl.tp_linear_rowwise_fp8(*x, *w)
+    want = ref.values(*x).cuda() @ ref.values(*w).cuda().t().contiguous()
+    assert torch.equal(y.double(), want)
+
+
+@pytest.mark.parametrize("m", [3, 60, 300])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_strided_operands_and_outputs(m, act):
+    """Operands are columns [512, 1280) of wider rows (scale columns [4, 10)), the output lies inside a
+    wider buffer whose other elements stay as they were."""
+    n = 96
+    g = torch.Generator().manual_seed(m)
+    rows = 2 * n if act == "swiglu" else n
+    xc, xs = _integers(g, m, 2048)
+    wc, ws = _integers(g, rows, 2048)
+    x, w = (xc[:, 512:1280], xs[:, 4:10]), (wc[:, 512:1280], ws[:, 4:10])
+    for out, pad in ((BF, 16), (F32, 8)):
+        buf = torch.full((m + 2, n + 2 * pad), 7.0, dtype=out, device="cuda")
+        y = tsl.tp_linear_colwise_fp8(*x, *w, act=act, out=buf[1:m + 1, pad:pad + n])
+        ref.check(y, *ref.linear(ref.values(*x), ref.values(*w), None, act))
+        buf[1:m + 1, pad:pad + n] = 7.0
+        assert (buf == 7).all()
+
+
+@pytest.mark.parametrize("m", [1, 20, 100, 260])
+def test_nan_blocks_reach_their_row_and_column_only(m):
+    """A NaN scale in one activation row and one weight row makes that output row and column NaN."""
+    g = torch.Generator().manual_seed(m)
+    n, k = 144, 512
+    xv, wv = torch.randn(m, k, generator=g), torch.randn(n, k, generator=g)
+    xv[m // 2, 300] = float("inf")
+    wv[77, 5] = float("nan")
+    x, w = tsl.tp_quantize_fp8(xv.cuda()), tsl.tp_quantize_fp8(wv.cuda())
+    y = tsl.tp_linear_colwise_fp8(*x, *w, out_dtype=F32).cpu()
+    want = torch.zeros(m, n, dtype=torch.bool)
+    want[m // 2] = True
+    want[:, 77] = True
+    assert torch.equal(torch.isnan(y), want)
+
+
+@pytest.mark.parametrize("m", [1, 40, 300])
+def test_scales_over_their_whole_range(m):
+    """Scales 2^-60 .. 2^60 whose products stay within fp32: the scale of each block counts."""
+    g = torch.Generator().manual_seed(5)
+    n, k = 64, 512
+    xc = torch.randint(1, 5, (m, k), generator=g).float().to(torch.float8_e4m3fn)
+    wc = torch.randint(1, 5, (n, k), generator=g).float().to(torch.float8_e4m3fn)
+    e = torch.tensor([-60, 60, -20, 33])
+    x = _pair(xc, (127 + e).to(torch.uint8).expand(m, 4).contiguous())
+    w = _pair(wc, (127 - e + torch.randint(-2, 3, (n, 4), generator=g)).to(torch.uint8))
+    y = tsl.tp_linear_rowwise_fp8(*x, *w)
+    ref.check(y, *ref.linear(ref.values(*x), ref.values(*w), None, "none"))
+
+
+def test_no_rows_is_a_no_op():
+    w = _integers(torch.Generator().manual_seed(0), 32, 256)
+    x = tsl.tp_quantize_fp8(torch.empty(0, 256, dtype=BF, device="cuda"))
+    assert tsl.tp_linear_colwise_fp8(*x, *w).shape == (0, 32)
+    assert tsl.tp_linear_rowwise_fp8(*x, *w).shape == (0, 32)
+
+
+def test_rowwise_shards_sum_to_the_whole_product():
+    """Quantized rows cut at multiples of 512 features: the partials of the cuts add up to the whole."""
+    g = torch.Generator().manual_seed(9)
+    x, w = _integers(g, 200, 2048), _integers(g, 160, 2048)
+    whole = tsl.tp_linear_rowwise_fp8(*x, *w)
+    parts = [tsl.tp_linear_rowwise_fp8(*(t[:, 512 * r // d:512 * (r + 1) // d] for t, d in
+                                         ((x[0], 1), (x[1], 128), (w[0], 1), (w[1], 128)))) for r in range(4)]
+    assert torch.equal(tsl.tp_partial_combine(parts, "sum"), whole)
+
+
+def test_repeated_calls_give_the_same_bits():
+    g = torch.Generator().manual_seed(11)
+    for m in (1, 30, 120, 500):
+        x, w = _normal(g, m, 1536), _normal(g, 400, 1536)
+        first = tsl.tp_linear_rowwise_fp8(*x, *w)
+        for _ in range(3):
+            assert torch.equal(tsl.tp_linear_rowwise_fp8(*x, *w), first)
