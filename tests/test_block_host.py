@@ -140,9 +140,12 @@ def test_norm_refusals(kw, status):
 
 @pytest.mark.parametrize("parts,kw", [
     ([A], dict(h=None)), ([A], dict(ldh=255)), ([A], dict(h=A + 1)), ([A], dict(ld_part=255)), ([None], {}), ([A, A + 2], {}),
-    ([A], dict(parts=None)), ([A], dict(post_weight=A)), ([A], dict(pre_norm=0)),
+    ([A], dict(parts_null=True)), ([A], dict(post_weight=A)), ([A], dict(pre_norm=0)),
     ([A], dict(pre_norm=0, z=None, pre_bias=A)), ([A], dict(MOD, pre_norm=0, z=None)), ([A], dict(bias=A + 1))])
 def test_norm_refusals_with_parts(parts, kw):
+    if kw.pop("parts_null", False):
+        kw = dict(num_parts=1, ld_part=256, h=A, ldh=256)
+        parts = None
     assert norm(parts, **kw) == INV
     assert tsl.tp_last_error().startswith("tp_block_norm")
 
