@@ -71,6 +71,8 @@ __global__ __launch_bounds__(256) void gemm_fp8_kernel(Fp8Problem p)
 
 hipError_t launch_gemm_fp8(const Fp8Problem &p, hipStream_t stream)
 {
+    if (p.out_bf16 && p.M > 128)
+        return launch_gemm_fp8_tiled(p, stream);
     const int64_t tiles = p.N / 16 * ((p.M + 15) / 16);
     hipLaunchKernelGGL(gemm_fp8_kernel, dim3((unsigned)((tiles + 3) / 4)), dim3(256), 0, stream, p);
     return hipGetLastError();

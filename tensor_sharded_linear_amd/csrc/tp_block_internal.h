@@ -77,6 +77,7 @@ struct Fp8Problem {
     int64_t M, N, K;
     bool out_bf16, gelu, swiglu;
 };
+hipError_t launch_gemm_fp8_tiled(const Fp8Problem &p, hipStream_t stream);
 hipError_t launch_gemm_fp8(const Fp8Problem &p, hipStream_t stream);
 
 // ---- block boundary ---------------------------------------------------------------------

@@ -41,6 +41,8 @@ def test_exact_on_small_integers(m, n, k):
     y = tsl.tp_linear_rowwise_fp8(*x, *w)
     want = ref.values(*x) @ ref.values(*w).t()
     assert torch.equal(y.cpu().double(), want)
+    y = tsl.tp_linear_colwise_fp8(*x, *w)                   # bf16: the exact sum, rounded once
+    assert torch.equal(y.cpu(), want.float().to(BF))
 
 
 @pytest.mark.parametrize("m", [1, 4, 16, 23, 64, 77, 128, 130, 333])
@@ -65,6 +67,7 @@ def test_many_tiles(m, n, k):
     y = tsl.tp_linear_rowwise_fp8(*x, *w)
     want = ref.values(*x).cuda() @ ref.values(*w).cuda().t().contiguous()
     assert torch.equal(y.double(), want)
+    assert torch.equal(tsl.tp_linear_colwise_fp8(*x, *w), want.float().to(BF))
 
 
 @pytest.mark.parametrize("m", [3, 60, 300])
