@@ -10,7 +10,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRow = 128;  // bytes of a row in an LDS tile: one scale block
 constexpr int kThreads8 = 256;
-typedef uint32_t __attribute__((aligned(1))) unaligned_u32;
 
 struct Fp8Params {
     const uint8_t *x, *w, *xs, *ws;
@@ -39,6 +38,24 @@ __device__ __forceinline__ void dma4_sbase(const char *base, uint32_t off, char 
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop
+
+// acc += 2^(sw + sx - 254) w . x^T over 128 features, the scales byte BYTE of sw and sx.
+template <int BYTE>
+__device__ __forceinline__ void scaled_mfma(f32x4 &acc, const i32x8 &w, const i32x8 &x, uint32_t sw, uint32_t sx)
+{
+#define TPL_SCALED_MFMA(SEL)                                                                               \
+    asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " SEL                            \
+                 : "+a"(acc) : "v"(w), "v"(x), "v"(sw), "v"(sx) : "memory")
+    if constexpr (BYTE == 0)
+        TPL_SCALED_MFMA("op_sel:[0,0,0] op_sel_hi:[0,0,0]");
+    else if constexpr (BYTE == 1)
+        TPL_SCALED_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+    else if constexpr (BYTE == 2)
+        TPL_SCALED_MFMA("op_sel:[0,0,0] op_sel_hi:[1,1,0]");
+    else
+        TPL_SCALED_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#undef TPL_SCALED_MFMA
+}
 
 template <int NXB, int NWB, bool GATED>
 __device__ __forceinline__ void mainloop8(const Fp8Params &p, uint16_t *lds, const Ctx &c, int m0, int n0,
@@ -113,11 +130,8 @@ __device__ __forceinline__ void mainloop8(const Fp8Params &p, uint16_t *lds, con
         dma4_sbase(reinterpret_cast<const char *>(p.ws) + 4 * group, wsoff, d + 1024);
     };
     const char *xsl = sl + (c.wave_m * WM + fr) * 4, *wsl = sl + 1024 + (c.wave_n * WN + fr) * 4;
-    auto sofs = [](int u) { return ((u >> 2) & 1) * 2048 + (u & 3); };
-    // the byte wanted and the three after it, which the MFMA does not look at: a byte load would be
-    // followed by a mask instruction right before the MFMA that uses it
-    auto scale = [](const char *t, int ofs, int block) {
-        return *reinterpret_cast<const unaligned_u32 *>(t + ofs + block * 64);
+    auto scale = [](const char *t, int buf, int block) {
+        return *reinterpret_cast<const uint32_t *>(t + buf * 2048 + block * 64);
     };
     const int groups = (T + 3) / 4;
     uint32_t sx[NXB], sw[NWB];
@@ -153,22 +167,19 @@ __device__ __forceinline__ void mainloop8(const Fp8Params &p, uint16_t *lds, con
     for (int d = 0; d < kF; ++d)
         dma(d, -1);
     int t = 0;
-    // k-tile t, whose parity is PAR
-    auto body = [&](i32x8 (&cur)[NXB], i32x8 (&nxt)[NXB], auto PAR) __attribute__((always_inline)) {
-        constexpr int par = decltype(PAR)::value;
+    // k-tile t, with S = t % 4
+    auto body = [&](i32x8 (&cur)[NXB], i32x8 (&nxt)[NXB], auto S) __attribute__((always_inline)) {
+        constexpr int st = decltype(S)::value, par = st & 1;
         const char *xn = xl + (par ^ 1) * kXBytes;          // X of k-tile t + 1
         const char *wc = wl + par * kWBytes, *wn = wl + (par ^ 1) * kWBytes;
-        const int sc = sofs(t), sn1 = sofs(t + 1);
+        const int buf = (t >> 2) & 1;  // of this k-tile's scales
         each([&](auto Q) __attribute__((always_inline)) {
             constexpr int q = decltype(Q)::value, j = q / NXB, i = q % NXB;
             if constexpr (q == kLast) {
                 wait_dma_keep<0>();
                 barrier_only();
             }
-            asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
-                         : "+a"(acc[i][j])
-                         : "v"(fw[j & 1]), "v"(cur[i]), "v"(sw[j]), "v"(sx[i])
-                         : "memory");
+            scaled_mfma<st>(acc[i][j], fw[j & 1], cur[i], sw[j], sx[i]);
             // loads: the rest of the step after the previous barrier, then the first of this one's
             if constexpr (q < kLast) {
                 if constexpr (q % DS == 0 && kF + q / DS < kDma)
@@ -185,19 +196,17 @@ __device__ __forceinline__ void mainloop8(const Fp8Params &p, uint16_t *lds, con
                 else
                     set(fw[0], i - 1, read(wn, 0, i - 1));
             }
-            // scales of the next k-tile, each after the last use of this one's
-            if constexpr (q == 0)
-                sx[NXB - 1] = scale(xsl, sc, NXB - 1);
-            if constexpr (q == 4)
-                sw[NWB - 1] = scale(wsl, sc, NWB - 1);
-            if constexpr (q > kLast)
-                sx[i - 1] = scale(xsl, sn1, i - 1);
-            if constexpr (j > 0 && i == 4)
-                sw[j - 1] = scale(wsl, sn1, j - 1);
-            if constexpr (q == NXB) {
-                if ((t & 3) == 1)
-                    dma_scales(min(t / 4 + 1, groups - 1));
-            }
+            // scales of the next four k-tiles, each after the last use of these
+            if constexpr (st == 0 && q == 0)
+                sx[NXB - 1] = scale(xsl, buf, NXB - 1);
+            if constexpr (st == 0 && q == 4)
+                sw[NWB - 1] = scale(wsl, buf, NWB - 1);
+            if constexpr (st == 3 && q > kLast)
+                sx[i - 1] = scale(xsl, buf ^ 1, i - 1);
+            if constexpr (st == 3 && j > 0 && i == 4)
+                sw[j - 1] = scale(wsl, buf ^ 1, j - 1);
+            if constexpr (st == 1 && q == NXB)
+                dma_scales(min(t / 4 + 1, groups - 1));
         }, std::make_integer_sequence<int, kMfma>{});
     };
     for (;;) {
@@ -205,6 +214,12 @@ __device__ __forceinline__ void mainloop8(const Fp8Params &p, uint16_t *lds, con
         if (++t == T)
             break;
         body(fb, fa, std::integral_constant<int, 1>{});
+        if (++t == T)
+            break;
+        body(fa, fb, std::integral_constant<int, 2>{});
+        if (++t == T)
+            break;
+        body(fb, fa, std::integral_constant<int, 3>{});
         if (++t == T)
             break;
     }
@@ -223,7 +238,7 @@ void gemm_fp8_nt_kernel(Fp8Params p)
 {
     constexpr bool kGated = ACT == kActSwiglu;
     constexpr int BM = 32 * NXB, BN = 32 * NWB, kTileCols = kGated ? BN / 2 : BN;
-    __shared__ __attribute__((aligned(1024))) uint16_t lds[(BM + BN) * kRow + 2048 + 8];  // two stages, two scale groups and 3 bytes read past them
+    __shared__ __attribute__((aligned(1024))) uint16_t lds[(BM + BN) * kRow + 2048];  // two stages, two scale groups
     Ctx c;
     c.lane = threadIdx.x & 63;
     c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
