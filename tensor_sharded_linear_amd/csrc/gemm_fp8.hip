@@ -1,81 +1,69 @@
-// gemm_fp8.hip -- Y = epilogue(X . W^T) on quantized rows (e4m3 codes, e8m0 scale per 128 features).
+// gemm_fp8.hip -- which kernel runs a product of quantized rows (e4m3 codes, e8m0 scale per 128
+// features):
 //
 //   y[m, n] = sum_b 2^(sx[m,b] + sw[n,b]) sum_{k in block b} x[m,k] w[n,k]
 //
-// One v_mfma_scale_f32_16x16x128_f8f6f4 covers 16 rows of each operand and one scale block of
-// 128 features, and multiplies the products by both rows' scales inside the matrix core: each
-// lane passes the scale byte of the operand row that it holds.
+// Few rows take the split-K kernel (gemm_fp8_narrow.hip), a few hundred rows the eight-wave tiles
+// (gemm_fp8_small.hip), more the four-wave tiles (gemm_fp8_tiled.hip).
 #include "tp_block_internal.h"
 
 namespace tpl {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+// Tiles for more than kFp8NarrowMaxM rows: the candidate with the least
+// (0.2 r + 0.8 ceil r) x (time of a k-tile), r = rounds of tiles over the CUs, at least 1 (a partly
+// filled last round runs a little faster than a full one).  The times, in us at low load, and the
+// choice were checked against sweeps of every shape.  bf16 output (8-bit products; 17 products of
+// 512 to 8192 rows, K 640 to 8192): the choice is within 0.5% of the fastest shape; 4608 x 9216 x 6144
+// takes 224 x 256 (2.95 rounds, 184 us against 190 in 256 x 256), 4608 x 4608 x 6144 224 x 192 (1.97
+// rounds, 116 against 144), 8192^3 256 x 256 (369 against 393 to 471).  fp32 output (exact products):
+// 4608 x 6144 x 4608 takes 224 x 256 (174 us against 183 in 256 x 256 and 182 in 192 x 192), 1024 x
+// 4608 x 6144 192 x 192 (67 against 97 to 108 and 88 in 128 x 128).  The eight-wave tiles of 128 and 64 rows
+// by 128 columns run the few hundred rows that leave most CUs idle otherwise: 333 x 6144 x 4608 43 us
+// in 128 x 128 against 52 in 192 x 192, 129 x 4608 x 6144 38 us in 64 x 128.
+struct TileChoice {
+    int nxb, nwb;  // nwb == 2: the eight-wave kernel
+};
 
-__device__ __forceinline__ float gelu_tanh(float v)
+TileChoice pick_tile(const Fp8Problem &p)
 {
-    const float a = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
-    const float b = 0.044715f * a;
-    const float e = __builtin_amdgcn_exp2f(v * __builtin_fmaf(b, v * v, a));
-    return v * __builtin_amdgcn_rcpf(1.0f + e);
-}
-
-__device__ __forceinline__ float silu(float v)
-{
-    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
-}
-
-// One wave per 16 x 16 outputs (and the matching up rows): operands straight from memory.
-__global__ __launch_bounds__(256) void gemm_fp8_kernel(Fp8Problem p)
-{
-    const int lane = threadIdx.x & 63;
-    const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t tn = p.N / 16, tm = (p.M + 15) / 16;
-    if (tile >= tn * tm)
-        return;
-    const int64_t n0 = tile % tn * 16, m0 = tile / tn * 16;
-    const int64_t xr = min(m0 + (lane & 15), p.M - 1), wr = n0 + (lane & 15);
-    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
-    const int halves = p.swiglu ? 2 : 1;
-    for (int64_t b = 0; b < p.K / kQBlock; ++b) {
-        const int64_t k = b * kQBlock + 32 * (lane >> 4);
-        const i32x8 fx = *(const i32x8 *)(p.x + xr * p.ldx + k);
-        const int sx = p.xs[xr * p.ldxs + b];
-        for (int h = 0; h < halves; ++h) {
-            const i32x8 fw = *(const i32x8 *)(p.w + (wr + h * p.N) * p.ldw + k);
-            const int sw = p.ws[(wr + h * p.N) * p.ldws + b];
-            acc[h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fw, fx, acc[h], 0, 0, 0, sw, 0, sx);
+    struct Cand {
+        int nxb, nwb;
+        double time;
+    };
+    static const Cand kEight[] = {{8, 8, 1.15}, {7, 8, 1.01}, {7, 6, 0.89}, {6, 6, 0.76}, {4, 2, 1.18}, {2, 2, 0.78}};
+    static const Cand kEightGated[] = {{8, 8, 1.15}, {7, 8, 1.01}, {6, 8, 0.93}, {4, 2, 1.18}, {2, 2, 0.78}};
+    static const Cand kExact[] = {{8, 8, 2.31}, {7, 8, 2.07}, {6, 6, 1.43}, {4, 2, 1.18}, {2, 2, 0.78}};
+    static const Cand kExactGated[] = {{8, 8, 2.31}, {7, 8, 2.07}, {4, 2, 1.18}, {2, 2, 0.78}};
+    const Cand *first = p.out_bf16 ? (p.swiglu ? kEightGated : kEight) : (p.swiglu ? kExactGated : kExact);
+    const int count = p.out_bf16 ? (p.swiglu ? 5 : 6) : (p.swiglu ? 4 : 5);
+    const int cus = cu_count();
+    TileChoice best{8, 8};
+    double best_cost = -1;
+    for (const Cand *c = first; c < first + count; ++c) {
+        const int bm = 32 * c->nxb, bn = c->nwb == 2 ? 128 : 32 * c->nwb, cols = p.swiglu ? bn / 2 : bn;
+        const int64_t tiles = (p.M + bm - 1) / bm * ((p.N + cols - 1) / cols);
+        if (tiles > ((int64_t)1 << 22))
+            continue;  // the launch's thread count must stay below 2^32 (256 x 256 always fits)
+        const double r = tiles < cus ? 1.0 : (double)tiles / cus;
+        const double cost = (0.2 * r + 0.8 * (double)((tiles + cus - 1) / cus)) * c->time;
+        if (best_cost < 0 || cost < best_cost) {
+            best = TileChoice{c->nxb, c->nwb};
+            best_cost = cost;
         }
     }
-    const int64_t m = m0 + (lane & 15), n = n0 + 4 * (lane >> 4);
-    if (m >= p.M)
-        return;
-    for (int i = 0; i < 4; ++i) {
-        float v = acc[0][i], u = acc[1][i];
-        if (p.bias) {
-            v += (float)((const __bf16 *)p.bias)[n + i];
-            if (p.swiglu)
-                u += (float)((const __bf16 *)p.bias)[p.N + n + i];
-        }
-        v = p.gelu ? gelu_tanh(v) : (p.swiglu ? silu(v) * u : v);
-        if (p.out_bf16)
-            ((__bf16 *)p.y)[m * p.ldy + n + i] = (__bf16)v;
-        else
-            ((float *)p.y)[m * p.ldy + n + i] = v;
-    }
+    return best;
 }
 
 }  // namespace
 
 hipError_t launch_gemm_fp8(const Fp8Problem &p, hipStream_t stream)
 {
-    if (p.out_bf16 && p.M > 128)
-        return launch_gemm_fp8_tiled(p, stream);
-    const int64_t tiles = p.N / 16 * ((p.M + 15) / 16);
-    hipLaunchKernelGGL(gemm_fp8_kernel, dim3((unsigned)((tiles + 3) / 4)), dim3(256), 0, stream, p);
-    return hipGetLastError();
+    if (p.M > kFp8NarrowMaxM) {
+        const TileChoice c = pick_tile(p);
+        return c.nwb == 2 ? launch_gemm_fp8_small(p, c.nxb, stream) : launch_gemm_fp8_tiled(p, c.nxb, c.nwb, stream);
+    }
+    return launch_gemm_fp8_narrow(p, stream);
 }
 
 }  // namespace tpl

@@ -1,0 +1,304 @@
+// gemm_fp8_narrow.hip -- product of quantized rows for few rows (up to 112): split-K, exact products.
+//
+// With few rows the weight stream sets the time: 9216 x 6144 codes and their scales are 57 MB, 7 us at
+// 8 TB/s.  So a workgroup of 4 waves owns all M rows, as MB blocks of 16, and a run of output columns
+// (weight rows, NB blocks of 16) sized so that every CU streams about the same number of them, and
+// its waves split K: wave w takes the scale blocks w, w + 4, ... of 128 features.  Wave w's step i then
+// needs byte w of the i-th dword of every scale row.
+//
+//  * Each wave feeds itself: a private LDS ring of D steps, filled by direct-to-LDS loads of whole
+//    128-byte lines (8 lanes a line), D - 1 steps in flight while one is computed, and no barrier.
+//    D fills the 160 KiB of LDS (8 steps for one row block and one column block, 2 for 7 and 2), which
+//    holds several times the bytes in flight that the registers of the wave could.
+//  * The fragments are read from LDS as 16-byte chunks (chunk c of row r at c ^ ((r >> 1) & 7)), widened
+//    to bf16 times their scale (exact) and multiplied by v_mfma_f32_16x16x32_bf16: few rows leave the
+//    matrix cores idle, so the products cost nothing by being exact, whatever the output type.
+//  * The waves' fp32 partial tiles meet in LDS and are added in wave order, so each output is the same
+//    sum whatever N is; one item per lane then applies bias, GELU or SwiGLU and rounding.
+#include <type_traits>
+
+#include "gemm_tile.h"
+#include "tp_block_internal.h"
+
+namespace tpl {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kThreadsN = 256;
+constexpr int kWavesN4 = 4;
+constexpr int kLdsBytes = 160 * 1024;
+
+struct NarrowParams {
+    const uint8_t *x, *w, *xs, *ws;
+    const uint16_t *bias;
+    void *y;
+    int64_t ldx, ldw, ldxs, ldws, ldy;
+    int M, N, K;
+    int rows;  // output columns per workgroup, a multiple of 4
+    bool gelu;
+};
+
+template <int MB, int NB>
+struct Ring {
+    static constexpr int kBlocks = NB + MB;
+    static constexpr int kScaleLoads = (kBlocks + 3) / 4;  // 64 rows each
+    static constexpr int kStep = kBlocks * 2048 + kScaleLoads * 256;
+    static constexpr int kLoads = 2 * kBlocks + kScaleLoads;  // per wave and step
+    static constexpr int kFit = kLdsBytes / (kWavesN4 * kStep);
+    static constexpr int kByCount = 60 / kLoads + 1;  // (D - 1) steps of loads fit the wait counter
+    static constexpr int D = kFit < kByCount ? (kFit < 8 ? kFit : 8) : (kByCount < 8 ? kByCount : 8);
+    static constexpr int kReduce = kWavesN4 * MB * NB * 1024;
+    static constexpr int kBytes = kWavesN4 * D * kStep > kReduce ? kWavesN4 * D * kStep : kReduce;
+    static_assert(D >= 2 && kBytes <= kLdsBytes, "two steps and the partial tiles fit in LDS");
+};
+
+// Four bytes a lane straight to LDS (lane l writes dst + 4 l), from the lane's own address.
+__device__ __forceinline__ void dma4_lane(const char *src, char *dst)
+{
+    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 4, 0, 0);
+}
+
+// Eight codes to bf16, times a power of two (exact).
+__device__ __forceinline__ bf16x8 widen8(int a, int b, float s)
+{
+    const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, false);
+    const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, true);
+    const bf16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, false);
+    const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, true);
+    return bf16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+}
+
+__device__ __forceinline__ f32x4 bias4(const uint16_t *b, int n)
+{
+    const bf16x4 v = *reinterpret_cast<const bf16x4 *>(b + n);
+    return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+
+// NB blocks of 16 weight rows cover the workgroup's p.rows output columns (GATED: block 0 the gate
+// rows, block 1 the matching up rows, p.rows <= 16).
+template <int MB, int NB, bool GATED, bool OUT_BF16>
+__global__ __launch_bounds__(kThreadsN) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void gemm_fp8_narrow_kernel(NarrowParams p)
+{
+    typedef Ring<MB, NB> R;
+    constexpr int D = R::D, kBlocks = R::kBlocks;
+    static_assert(!GATED || NB == 2, "the gated form pairs one gate and one up block");
+    __shared__ __attribute__((aligned(1024))) char lds[R::kBytes];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * p.rows, n_end = min(n0 + p.rows, p.N);
+    const int steps = (p.K / kQBlock - wave + kWavesN4 - 1) / kWavesN4;
+    char *ring = lds + wave * (D * R::kStep);
+    // Row r of block b, W blocks first; rows past the end repeat the last one.
+    const auto wrow = [&](int b, int r) {
+        return GATED ? b * p.N + min(n0 + r, n_end - 1) : min(n0 + 16 * b + r, n_end - 1);
+    };
+    const auto xrow = [&](int b, int r) { return min(16 * (b - NB) + r, p.M - 1); };
+    uint32_t off[kBlocks][2];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = 8 * h + (lane >> 3), chunk = (lane & 7) ^ ((r >> 1) & 7);
+            off[b][h] = b < NB ? (uint32_t)wrow(b, r) * (uint32_t)p.ldw + chunk * 16
+                               : (uint32_t)xrow(b, r) * (uint32_t)p.ldx + chunk * 16;
+        }
+    // Scale load s: lane l takes row l % 16 of block 4 s + l / 16; a lane's block is W or X, so its
+    // base differs, and the loads take 64-bit lane addresses.
+    const char *sptr[R::kScaleLoads];
+#pragma unroll
+    for (int s = 0; s < R::kScaleLoads; ++s) {
+        const int b = min(4 * s + (lane >> 4), kBlocks - 1), r = lane & 15;
+        sptr[s] = reinterpret_cast<const char *>(b < NB ? p.ws : p.xs) +
+                  (b < NB ? (uint32_t)wrow(b, r) * (uint32_t)p.ldws : (uint32_t)xrow(b, r) * (uint32_t)p.ldxs);
+    }
+    const char *xbase = reinterpret_cast<const char *>(p.x), *wbase = reinterpret_cast<const char *>(p.w);
+    // step i of the wave into ring slot `slot`; past the last step, the last one again
+    auto issue = [&](int i, int slot) {
+        const int u = min(i, steps - 1);
+        const int k = (u * kWavesN4 + wave) * kQBlock;
+        char *d = ring + slot * R::kStep;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                dma16_sbase((b < NB ? wbase : xbase) + k, off[b][h], reinterpret_cast<uint16_t *>(d + b * 2048 + h * 1024));
+#pragma unroll
+        for (int s = 0; s < R::kScaleLoads; ++s)
+            dma4_lane(sptr[s] + 4 * u, d + kBlocks * 2048 + s * 256);
+    };
+    f32x4 acc[MB][NB];
+    zero<MB, NB>(acc);
+    const int fr = lane & 15, g = lane >> 4, swz = (lane >> 1) & 7;
+    if (steps > 0) {
+#pragma unroll
+        for (int i = 0; i < D; ++i)
+            issue(i, i);
+        int slot = 0;
+        for (int i = 0; i < steps; ++i) {
+            wait_dma_keep<(D - 1) * R::kLoads>();
+            const char *s = ring + slot * R::kStep;
+            i32x4 raw[kBlocks][2];
+            float f[kBlocks];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    raw[b][h] = *reinterpret_cast<const i32x4 *>(s + b * 2048 + fr * 128 + ((4 * h + g) ^ swz) * 16);
+                const uint32_t d = *reinterpret_cast<const uint32_t *>(s + kBlocks * 2048 + (16 * b + fr) * 4);
+                // the scale byte as an fp32 exponent: all that the conversion looks at
+                f[b] = __uint_as_float((d >> (8 * wave)) << 23);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the slot has been read: refill it
+            issue(i + D, slot);
+            slot = slot == D - 1 ? 0 : slot + 1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                bf16x8 w[NB];
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+                    w[j] = widen8(raw[j][q / 2][q % 2 * 2], raw[j][q / 2][q % 2 * 2 + 1], f[j]);
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    const bf16x8 x = widen8(raw[NB + m][q / 2][q % 2 * 2], raw[NB + m][q / 2][q % 2 * 2 + 1], f[NB + m]);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], x, acc[m][j], 0, 0, 0);
+                }
+            }
+        }
+    }
+    wait_dma();       // the repeated loads of the last step
+    __syncthreads();  // every wave is done with its ring
+    f32x4 *red = reinterpret_cast<f32x4 *>(lds);
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            red[(wave * MB * NB + m * NB + j) * 64 + lane] = acc[m][j];
+    __syncthreads();
+    typedef typename std::conditional<OUT_BF16, __bf16, float>::type OutT;
+    // Item (block, l): lane l of every wave holds Y[16 m + l % 16][n .. n + 3], n = column base + 16 j +
+    // 4 (l / 16); n and n_end are multiples of 4.
+    constexpr int kItems = (GATED ? MB : MB * NB) * 64;
+    const auto total = [&](int blk, int l) {
+        f32x4 v = red[blk * 64 + l];
+#pragma unroll
+        for (int w = 1; w < kWavesN4; ++w)
+            v += red[(w * MB * NB + blk) * 64 + l];
+        return v;
+    };
+    for (int e = threadIdx.x; e < kItems; e += kThreadsN) {
+        const int l = e & 63, blk = GATED ? (e >> 6) * NB : e >> 6;
+        const int m = 16 * (blk / NB) + (l & 15), n = n0 + 16 * (blk % NB) + 4 * (l >> 4);
+        if (m >= p.M || n >= n_end)
+            continue;
+        f32x4 v = total(blk, l);
+        if (p.bias)
+            v += bias4(p.bias, n);
+        if (p.gelu) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = gelu_tanh(v[i]);
+        }
+        if (GATED) {
+            f32x4 u = total(blk + 1, l);
+            if (p.bias)
+                u += bias4(p.bias, p.N + n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = silu(v[i]) * u[i];
+        }
+        OutT *dst = reinterpret_cast<OutT *>(p.y) + (int64_t)m * p.ldy + n;
+        if (OUT_BF16)
+            *reinterpret_cast<bf16x4 *>(dst) = bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        else
+            *reinterpret_cast<f32x4 *>(dst) = v;
+    }
+}
+
+template <int MB, int NB, bool GATED>
+hipError_t launch_mb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
+{
+    const dim3 grid((np.N + np.rows - 1) / np.rows), block(kThreadsN);
+    if (out_bf16)
+        hipLaunchKernelGGL((gemm_fp8_narrow_kernel<MB, NB, GATED, true>), grid, block, 0, stream, np);
+    else
+        hipLaunchKernelGGL((gemm_fp8_narrow_kernel<MB, NB, GATED, false>), grid, block, 0, stream, np);
+    return hipGetLastError();
+}
+
+template <int NB, bool GATED>
+hipError_t launch_nb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
+{
+    switch ((np.M + 15) / 16) {
+    case 1: return launch_mb<1, NB, GATED>(np, out_bf16, stream);
+    case 2: return launch_mb<2, NB, GATED>(np, out_bf16, stream);
+    case 3: return launch_mb<3, NB, GATED>(np, out_bf16, stream);
+    case 4: return launch_mb<4, NB, GATED>(np, out_bf16, stream);
+    default:
+        if constexpr (NB <= 2) {
+            switch ((np.M + 15) / 16) {
+            case 5: return launch_mb<5, NB, GATED>(np, out_bf16, stream);
+            case 6: return launch_mb<6, NB, GATED>(np, out_bf16, stream);
+            default: return launch_mb<7, NB, GATED>(np, out_bf16, stream);
+            }
+        }
+        return hipErrorInvalidValue;  // pick_rows gives more than 64 rows at most two blocks
+    }
+}
+
+// Output columns per workgroup: the CUs share the weight stream, and every workgroup also reads all
+// of X (from L2; a line costs about 0.6 of a weight line from HBM).  The LDS ring leaves room for
+// one workgroup per CU, so the cost of a choice is ceil(workgroups / CUs) x (weight rows + 0.6 M).
+// Ties go to more columns per workgroup.
+int pick_rows(const Fp8Problem &p, int cus)
+{
+    const int max_rows = p.swiglu ? 16 : (p.M > 64 ? 32 : 48);
+    int best = 4;
+    double best_cost = -1;
+    for (int rows = 4; rows <= max_rows; rows += 4) {
+        const int64_t wgs = (p.N + rows - 1) / rows;
+        const double cost = (double)((wgs + cus - 1) / cus) * ((p.swiglu ? 2 : 1) * rows + 0.6 * (double)p.M);
+        if (best_cost < 0 || cost <= best_cost) {
+            best = rows;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+hipError_t launch_gemm_fp8_narrow(const Fp8Problem &pr, hipStream_t stream)
+{
+    NarrowParams np;
+    np.x = pr.x;
+    np.w = pr.w;
+    np.xs = pr.xs;
+    np.ws = pr.ws;
+    np.bias = pr.bias;
+    np.y = pr.y;
+    np.ldx = pr.ldx;
+    np.ldw = pr.ldw;
+    np.ldxs = pr.ldxs;
+    np.ldws = pr.ldws;
+    np.ldy = pr.ldy;
+    np.M = (int)pr.M;
+    np.N = (int)pr.N;
+    np.K = (int)pr.K;
+    np.rows = pick_rows(pr, cu_count());
+    np.gelu = pr.gelu;
+    if (pr.swiglu)
+        return launch_nb<2, true>(np, pr.out_bf16, stream);
+    switch ((np.rows + 15) / 16) {
+    case 1: return launch_nb<1, false>(np, pr.out_bf16, stream);
+    case 2: return launch_nb<2, false>(np, pr.out_bf16, stream);
+    default: return launch_nb<3, false>(np, pr.out_bf16, stream);
+    }
+}
+
+}  // namespace tpl

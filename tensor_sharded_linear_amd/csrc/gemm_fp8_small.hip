@@ -1,0 +1,229 @@
+// gemm_fp8_small.hip -- tiled product of quantized rows for a few hundred rows, eight waves.
+#include "gemm_tile.h"
+#include "tp_block_internal.h"
+
+namespace tpl {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kRow = 128;         // bytes of a row in an LDS tile: one scale block
+constexpr int kThreadsS = 512;    // 8 waves in a 2 (M) x 4 (N) grid
+
+struct SmallParams {
+    const uint8_t *x, *w, *xs, *ws;
+    const uint16_t *bias;
+    void *y;
+    int64_t ldx, ldw, ldxs, ldws, ldy;
+    int M, N, K;
+    int tiles_m, tiles_n, group_m;
+};
+
+template <int NXB, int NWB>
+struct STile {
+    static constexpr int WM = 16 * NXB, WN = 16 * NWB, BM = 2 * WM, BN = 4 * WN;
+    static constexpr int kStageBytes = (BM + BN) * kRow;
+    static constexpr int kFit = (160 * 1024 - 4096) / kStageBytes;
+    static constexpr int kStages = kFit > 5 ? 5 : kFit;
+    static constexpr int kLdsBytes = kStages * kStageBytes + 4096;
+};
+
+// A scale byte as an fp32 exponent: all that the conversion below looks at (255 is NaN, 0 is 2^-127).
+__device__ __forceinline__ float factor(uint32_t dword, int u) { return __uint_as_float((dword >> (8 * (u & 3))) << 23); }
+
+// Eight codes to bf16, times a power of two (exact).
+__device__ __forceinline__ bf16x8 widen8(int a, int b, float s)
+{
+    const bf16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, false);
+    const bf16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, s, true);
+    const bf16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, false);
+    const bf16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, s, true);
+    return bf16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+}
+
+__device__ __forceinline__ void dma_to_lds16(const char *src, char *dst)
+{
+    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+__device__ __forceinline__ void dma_to_lds4(const char *src, char *dst)
+{
+    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 4, 0, 0);
+}
+
+template <int NXB, int NWB, bool GATED>
+__device__ __forceinline__ void mainloop_small(const SmallParams &p, char *lds, const Ctx &c, int m0, int n0,
+                                               f32x4 (&acc)[NXB][NWB])
+{
+    typedef STile<NXB, NWB> L;
+    constexpr int BM = L::BM, BN = L::BN, S = L::kStages;
+    constexpr int kDmaX = BM / 64, kDmaW = BN / 64, kPer = kDmaX + kDmaW;
+    static_assert(S >= 2 && (S - 2) * kPer <= 60, "the wait count fits vmcnt");
+    // weight row of a tile row; gated: a wave column's first half holds gate rows, its second up rows
+    auto wrow = [&](int r) {
+        if (!GATED)
+            return min(n0 + r, p.N - 1);
+        const int q = r / L::WN, o = r % L::WN;
+        return (o / (L::WN / 2)) * p.N + min(n0 + q * (L::WN / 2) + o % (L::WN / 2), p.N - 1);
+    };
+    const int dma_row = c.wave * 8 + (c.lane >> 3);
+    const int dma_chunk = (c.lane & 7) ^ ((((c.wave & 1) << 2) + (c.lane >> 4)) & 7);
+    uint32_t off[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        off[j] = j < kDmaX ? (uint32_t)min(m0 + 64 * j + dma_row, p.M - 1) * (uint32_t)p.ldx + dma_chunk * 16
+                           : (uint32_t)wrow(64 * (j - kDmaX) + dma_row) * (uint32_t)p.ldw + dma_chunk * 16;
+    const int T = p.K / kRow, groups = (T + 3) / 4;
+    const char *xbase = reinterpret_cast<const char *>(p.x), *wbase = reinterpret_cast<const char *>(p.w);
+    auto issue = [&](int u, int stage) {
+        const int k = min(u, T - 1) * kRow;
+        char *d = lds + stage * L::kStageBytes + c.wave * 1024;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            dma_to_lds16((j < kDmaX ? xbase : wbase) + k + off[j], d + j * 8192);
+    };
+    // Scales of four k-tiles, a dword a row: the X tile's rows, then the W tile's; two buffers.
+    char *sl = lds + S * L::kStageBytes;
+    const int srow = c.wave * 64 + c.lane;
+    const char *sbase = reinterpret_cast<const char *>(srow < BM ? p.xs : p.ws);
+    const uint32_t soff = srow < BM ? (uint32_t)min(m0 + srow, p.M - 1) * (uint32_t)p.ldxs
+                                    : (uint32_t)wrow(min(srow - BM, BN - 1)) * (uint32_t)p.ldws;
+    auto issue_scales = [&](int group) {
+        dma_to_lds4(sbase + 4 * min(group, groups - 1) + soff, sl + (group & 1) * 2048 + c.wave * 256);
+    };
+    issue_scales(0);
+#pragma unroll
+    for (int u = 0; u < S - 1; ++u)
+        issue(u, u);
+    const int fr = c.lane & 15, g = c.lane >> 4, swz = (c.lane >> 1) & 7;
+    const int xrow = c.wave_m * L::WM + fr, wr0 = c.wave_n * L::WN + fr;
+    int stage = 0;
+    for (int t = 0; t < T; ++t) {
+        // k-tile t has landed (the S - 2 k-tiles after it stay in flight), and k-tile t - 1 has been
+        // read by every wave, so its stage takes k-tile t + S - 1.  The scales of a group are
+        // issued at its predecessor's first k-tile: at least three k-tiles of loads later they
+        // are behind every wait that leaves at most S - 2 <= 3 k-tiles in flight.
+        wait_dma_keep<(S - 2) * kPer>();
+        barrier_only();
+        issue(t + S - 1, stage == 0 ? S - 1 : stage - 1);
+        if ((t & 3) == 0)
+            issue_scales((t >> 2) + 1);
+        const char *xs = lds + stage * L::kStageBytes, *ws = xs + BM * kRow;
+        const char *sc = sl + ((t >> 2) & 1) * 2048;
+        float sx[NXB], sw[NWB];
+#pragma unroll
+        for (int i = 0; i < NXB; ++i)
+            sx[i] = factor(*reinterpret_cast<const uint32_t *>(sc + (xrow + 16 * i) * 4), t);
+#pragma unroll
+        for (int j = 0; j < NWB; ++j)
+            sw[j] = factor(*reinterpret_cast<const uint32_t *>(sc + (BM + wr0 + 16 * j) * 4), t);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int cpos = ((4 * h + g) ^ swz) * 16;
+            i32x4 rx[NXB], rw[NWB];
+#pragma unroll
+            for (int j = 0; j < NWB; ++j)
+                rw[j] = *reinterpret_cast<const i32x4 *>(ws + (wr0 + 16 * j) * kRow + cpos);
+#pragma unroll
+            for (int i = 0; i < NXB; ++i)
+                rx[i] = *reinterpret_cast<const i32x4 *>(xs + (xrow + 16 * i) * kRow + cpos);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                bf16x8 fw[NWB];
+#pragma unroll
+                for (int j = 0; j < NWB; ++j)
+                    fw[j] = widen8(rw[j][2 * s], rw[j][2 * s + 1], sw[j]);
+#pragma unroll
+                for (int i = 0; i < NXB; ++i) {
+                    const bf16x8 fx = widen8(rx[i][2 * s], rx[i][2 * s + 1], sx[i]);
+#pragma unroll
+                    for (int j = 0; j < NWB; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[j], fx, acc[i][j], 0, 0, 0);
+                }
+            }
+        }
+        stage = stage == S - 1 ? 0 : stage + 1;
+    }
+    wait_dma();  // the repeated loads of the last k-tile, before the epilogue reuses the LDS
+}
+
+template <int NXB, int NWB, bool OUT_BF16, bool HAS_BIAS, int ACT>
+__global__ __launch_bounds__(kThreadsS) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void gemm_fp8_small_kernel(SmallParams p)
+{
+    typedef STile<NXB, NWB> L;
+    constexpr bool kGated = ACT == kActSwiglu;
+    constexpr int kTileCols = kGated ? L::BN / 2 : L::BN;
+    __shared__ __attribute__((aligned(1024))) char lds[L::kLdsBytes];
+    Ctx c;
+    c.lane = threadIdx.x & 63;
+    c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    c.wave_m = c.wave >> 2;
+    c.wave_n = c.wave & 3;
+    int tm, tn;
+    tile_of(xcd_contiguous(blockIdx.x, p.tiles_m * p.tiles_n), p, tm, tn);
+    f32x4 acc[NXB][NWB];
+    zero<NXB, NWB>(acc);
+    mainloop_small<NXB, NWB, kGated>(p, lds, c, tm * L::BM, tn * kTileCols, acc);
+    epilogue<NXB, NWB, OUT_BF16, HAS_BIAS, ACT>(p, reinterpret_cast<uint16_t *>(lds), c, tm * L::BM, tn * kTileCols, acc);
+}
+
+template <int NXB, int NWB, bool OUT_BF16, bool HAS_BIAS, int ACT>
+hipError_t launch_tile(SmallParams gp, hipStream_t stream)
+{
+    typedef STile<NXB, NWB> L;
+    const int cols = ACT == kActSwiglu ? L::BN / 2 : L::BN;
+    gp.tiles_n = (gp.N + cols - 1) / cols;
+    gp.tiles_m = (gp.M + L::BM - 1) / L::BM;
+    gp.group_m = gp.tiles_m < 8 ? gp.tiles_m : 8;
+    hipLaunchKernelGGL((gemm_fp8_small_kernel<NXB, NWB, OUT_BF16, HAS_BIAS, ACT>), dim3(gp.tiles_m * gp.tiles_n),
+                       dim3(kThreadsS), 0, stream, gp);
+    return hipGetLastError();
+}
+
+template <bool OUT_BF16, bool HAS_BIAS, int ACT>
+hipError_t launch_shape(const SmallParams &gp, int nxb, hipStream_t stream)
+{
+    return nxb == 2 ? launch_tile<2, 2, OUT_BF16, HAS_BIAS, ACT>(gp, stream)
+                    : launch_tile<4, 2, OUT_BF16, HAS_BIAS, ACT>(gp, stream);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_fp8_small(const Fp8Problem &pr, int nxb, hipStream_t stream)
+{
+    SmallParams gp;
+    gp.x = pr.x;
+    gp.w = pr.w;
+    gp.xs = pr.xs;
+    gp.ws = pr.ws;
+    gp.bias = pr.bias;
+    gp.y = pr.y;
+    gp.ldx = pr.ldx;
+    gp.ldw = pr.ldw;
+    gp.ldxs = pr.ldxs;
+    gp.ldws = pr.ldws;
+    gp.ldy = pr.ldy;
+    gp.M = (int)pr.M;
+    gp.N = (int)pr.N;
+    gp.K = (int)pr.K;
+    const int act = pr.swiglu ? kActSwiglu : (pr.gelu ? kActGelu : kActNone);
+    switch ((pr.out_bf16 ? 6 : 0) + (pr.bias ? 3 : 0) + act) {
+    case 0: return launch_shape<false, false, 0>(gp, nxb, stream);
+    case 1: return launch_shape<false, false, 1>(gp, nxb, stream);
+    case 2: return launch_shape<false, false, 2>(gp, nxb, stream);
+    case 3: return launch_shape<false, true, 0>(gp, nxb, stream);
+    case 4: return launch_shape<false, true, 1>(gp, nxb, stream);
+    case 5: return launch_shape<false, true, 2>(gp, nxb, stream);
+    case 6: return launch_shape<true, false, 0>(gp, nxb, stream);
+    case 7: return launch_shape<true, false, 1>(gp, nxb, stream);
+    case 8: return launch_shape<true, false, 2>(gp, nxb, stream);
+    case 9: return launch_shape<true, true, 0>(gp, nxb, stream);
+    case 10: return launch_shape<true, true, 1>(gp, nxb, stream);
+    default: return launch_shape<true, true, 2>(gp, nxb, stream);
+    }
+}
+
+}  // namespace tpl

@@ -142,7 +142,7 @@ __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const C
     __syncthreads();  // every wave is done reading the operand stages
     typedef typename std::conditional<OUT_BF16, __bf16, float>::type OutT;
     constexpr bool kGated = ACT == kActSwiglu;
-    static_assert(!kGated || NWB == 4 || NWB == 8, "the gated epilogue pairs NWB / 2 gate and up blocks");
+    static_assert(!kGated || NWB % 2 == 0, "the gated epilogue pairs NWB / 2 gate and up blocks");
     constexpr int WNO = kGated ? 8 * NWB : 16 * NWB;  // output columns per wave
     constexpr int JO = WNO / 16;               // 16-column output blocks per wave
     constexpr int kOutEs = sizeof(OutT);
@@ -165,7 +165,7 @@ __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const C
     // When a pass of 64 lanes covers whole rows, each lane keeps its row and column for
     // every pass; otherwise (48 output columns per wave) a lane's position moves per pass.
     constexpr bool kWholeRows = 64 % kVecPerRow == 0;
-    constexpr int kRowsPerPass = kWholeRows ? 64 / kVecPerRow : 1;
+    constexpr int kRowsPerPass = kWholeRows ? 64 / kVecPerRow : 1;  // over 16: lanes past row 15 sit out
     constexpr int kPasses = (16 * kVecPerRow + 63) / 64;
     const int rd_row = lane / kVecPerRow;
     const int rd_vec = lane % kVecPerRow;
@@ -207,10 +207,11 @@ __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const C
             const bool col_ok = n0 + c.wave_n * WNO + rd_vec * kVec < p.N;
 #pragma unroll
             for (int r = 0; r < 16; r += kRowsPerPass) {
-                const f32x4 v = *reinterpret_cast<const f32x4 *>(stage + (r + rd_row) * kRowElems + rd_vec * kVec);
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(stage + (r + (kRowsPerPass <= 16 ? rd_row : (rd_row & 15))) * kRowElems +
+                                                                 rd_vec * kVec);
                 // Non-temporal stores: about 1% faster than ordinary ones over a DiT block's
                 // GEMMs, with the same fetched and written bytes.
-                if (rd_row < p.M - (mbase + r) && col_ok)
+                if ((kRowsPerPass <= 16 || rd_row < 16) && rd_row < p.M - (mbase + r) && col_ok)
                     __builtin_nontemporal_store(v, reinterpret_cast<f32x4 *>(ybase + (int64_t)(mbase + r) * p.ldy + lane_off));
             }
         } else {

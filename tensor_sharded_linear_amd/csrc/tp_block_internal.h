@@ -77,8 +77,14 @@ struct Fp8Problem {
     int64_t M, N, K;
     bool out_bf16, gelu, swiglu;
 };
-hipError_t launch_gemm_fp8_tiled(const Fp8Problem &p, hipStream_t stream);
 hipError_t launch_gemm_fp8(const Fp8Problem &p, hipStream_t stream);
+
+// Up to this many rows the kernel for few rows runs.
+constexpr int64_t kFp8NarrowMaxM = 112;
+hipError_t launch_gemm_fp8_narrow(const Fp8Problem &p, hipStream_t stream);
+// Four-wave tiles of 32 nxb x 32 nwb; eight-wave tiles of 32 nxb x 128.
+hipError_t launch_gemm_fp8_tiled(const Fp8Problem &p, int nxb, int nwb, hipStream_t stream);
+hipError_t launch_gemm_fp8_small(const Fp8Problem &p, int nxb, hipStream_t stream);
 
 // ---- block boundary ---------------------------------------------------------------------
 constexpr int64_t kNormMaxD = 32768;

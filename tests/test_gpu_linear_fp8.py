@@ -105,6 +105,23 @@ def test_nan_blocks_reach_their_row_and_column_only(m):
     assert torch.equal(torch.isnan(y), want)
 
 
+@pytest.mark.parametrize("m", [1, 20, 100, 260])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_nan_scales_of_finite_codes(m, out):
+    """A scale byte of 255 is NaN whatever the codes: one block of a row of each operand."""
+    g = torch.Generator().manual_seed(m)
+    n, k = 48, 640
+    xc, wc = (torch.randn(r, k, generator=g).to(torch.float8_e4m3fn) for r in (m, n))
+    xs, ws = (torch.full((r, k // 128), 127, dtype=torch.uint8) for r in (m, n))
+    xs[m - 1, 3] = 255
+    ws[11, 4] = 255
+    y = tsl.tp_linear_colwise_fp8(*_pair(xc, xs), *_pair(wc, ws), out_dtype=out).cpu()
+    want = torch.zeros(m, n, dtype=torch.bool)
+    want[m - 1] = True
+    want[:, 11] = True
+    assert torch.equal(torch.isnan(y), want)
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_scales_over_their_whole_range(m):
     """Scales 2^-60 .. 2^60 whose products stay within fp32: the scale of each block counts."""
