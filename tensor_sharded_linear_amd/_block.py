@@ -11,12 +11,13 @@ K8 = K rounded up to a multiple of 128 (zero codes past K), scales ``[rows, K8 /
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Sequence
 
 import torch
 
 from . import _binding as _b
-from ._binding import _check, _dev2d, _ld, _ptr, _stream, _vec
+from ._binding import _check, _dev2d, _ld, _ptr, _vec
 
 BLOCK = 128
 CODES = torch.float8_e4m3fn
@@ -40,12 +41,17 @@ class _BlockNormArgs(ctypes.Structure):
         ("residual_scale", _F), ("eps", _F)]
 
 
+# The same layout for struct.pack: one call fills all fields, where setting 38 ctypes fields one by one
+# took longer than the kernel of a few rows runs.
+_PACK = struct.Struct("@qqPqiiPqiiPPPPqiiPPPqPqiiPPPqqqqqPff")
+assert _PACK.size == ctypes.sizeof(_BlockNormArgs)
+
 # Every symbol include/tp_block.h declares, with its ctypes signature.
 SIGNATURES = {
     "tp_quantize_fp8": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _I64, _I64, _P]),
     "tp_linear_colwise_fp8": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I64, _I64, _I64, _P]),
     "tp_linear_rowwise_fp8": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P]),
-    "tp_block_norm": (_I, [ctypes.POINTER(_BlockNormArgs), _P]),
+    "tp_block_norm": (_I, [_P, _P]),
 }
 
 _lib = None
@@ -63,18 +69,26 @@ def _library() -> ctypes.CDLL:
     return _lib
 
 
-def _call(fn, device, *args) -> None:
-    """Call an entry point with `device` current (the library launches on the current device)."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args))
+def _call(fn, x: torch.Tensor, stream, *args) -> None:
+    """Call an entry point on `stream` (default: the current one) with x's device current (the
+    library launches on the current device)."""
+    index = x.get_device()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args))
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
 
 
 def _same_device(x: torch.Tensor, **others: Optional[torch.Tensor]) -> None:
     for name, t in others.items():
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != x.get_device():
             raise ValueError(f"{name} is on {t.device}, not on {x.device}")
 
 
@@ -83,7 +97,7 @@ def _empty_codes(m: int, k: int, device):
     kb = -(-k // BLOCK)
     codes = torch.empty((m, kb * BLOCK), dtype=CODES, device=device)
     scales = torch.empty((m, -(-kb // 4) * 4), dtype=SCALES, device=device)
-    return codes, scales[:, :kb]
+    return codes, scales if kb % 4 == 0 else scales[:, :kb]
 
 
 def _codes(t: torch.Tensor, s: torch.Tensor, name: str, m: Optional[int] = None, k8: Optional[int] = None) -> None:
@@ -126,8 +140,8 @@ def tp_quantize_fp8(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
     else:
         _codes(codes, scales, "output", m, -(-k // BLOCK) * BLOCK)
         _same_device(x, codes=codes, scales=scales)
-    _call(lib.tp_quantize_fp8, x.device, x.data_ptr(), _ld(x), _DT[x.dtype], codes.data_ptr(), _ld(codes),
-          scales.data_ptr(), _lds(scales), m, k, _stream(stream, x))
+    _call(lib.tp_quantize_fp8, x, stream, x.data_ptr(), _ld(x), _DT[x.dtype], codes.data_ptr(), _ld(codes),
+          scales.data_ptr(), _lds(scales), m, k)
     return codes, scales
 
 
@@ -165,9 +179,9 @@ def tp_linear_colwise_fp8(x: torch.Tensor, x_scale: torch.Tensor, w_shard: torch
     if tuple(out.shape) != (m, n) or out.dtype not in _DT:
         raise ValueError(f"out must be [{m}, {n}] bf16 or fp32")
     _same_device(x, bias=bias, out=out)
-    _call(lib.tp_linear_colwise_fp8, x.device, x.data_ptr(), _ld(x), x_scale.data_ptr(), _lds(x_scale),
+    _call(lib.tp_linear_colwise_fp8, x, stream, x.data_ptr(), _ld(x), x_scale.data_ptr(), _lds(x_scale),
           w_shard.data_ptr(), _ld(w_shard), w_scale.data_ptr(), _lds(w_scale), _ptr(bias), out.data_ptr(), _ld(out),
-          _DT[out.dtype], a, m, n, k, _stream(stream, x))
+          _DT[out.dtype], a, m, n, k)
     return out
 
 
@@ -184,17 +198,17 @@ def tp_linear_rowwise_fp8(x_shard: torch.Tensor, x_scale: torch.Tensor, w_shard:
     if tuple(out.shape) != (m, n):
         raise ValueError(f"out must be [{m}, {n}]")
     _same_device(x_shard, out=out)
-    _call(lib.tp_linear_rowwise_fp8, x_shard.device, x_shard.data_ptr(), _ld(x_shard), x_scale.data_ptr(),
+    _call(lib.tp_linear_rowwise_fp8, x_shard, stream, x_shard.data_ptr(), _ld(x_shard), x_scale.data_ptr(),
           _lds(x_scale), w_shard.data_ptr(), _ld(w_shard), w_scale.data_ptr(), _lds(w_scale), out.data_ptr(), _ld(out),
-          m, n, k, _stream(stream, x_shard))
+          m, n, k)
     return out
 
 
-def _feature_vec(t: Optional[torch.Tensor], name: str, x: torch.Tensor) -> Optional[int]:
+def _feature_vec(t: Optional[torch.Tensor], name: str, x: torch.Tensor) -> int:
     if t is None:
-        return None
+        return 0
     _vec(t, name, x.shape[1])
-    if t.device != x.device:
+    if t.get_device() != x.get_device():
         raise ValueError(f"{name} is on {t.device}, not on {x.device}")
     return t.data_ptr()
 
@@ -230,9 +244,9 @@ def tp_block_norm(x: torch.Tensor, parts: Optional[Sequence[torch.Tensor]] = Non
         raise ValueError("x has no columns")
     if post_norm not in _NORMS or pre_norm not in _NORMS:
         raise ValueError("post_norm and pre_norm must be 'none', 'layer' or 'rms'")
-    a = _BlockNormArgs(M=m, D=d, x=x.data_ptr(), ldx=_ld(x), x_dtype=_DT[x.dtype], post_norm=_NORMS[post_norm],
-                       pre_norm=_NORMS[pre_norm], residual_scale=residual_scale, eps=eps)
+    index = x.get_device()
     h, z = x, None
+    part_array, num_parts, ldp, part_dt, h_args = None, 0, 0, 0, (0, 0, 0)
     if parts is not None:
         parts = list(parts)
         if not parts:
@@ -243,70 +257,73 @@ def tp_block_norm(x: torch.Tensor, parts: Optional[Sequence[torch.Tensor]] = Non
             raise TypeError(f"parts must be bf16 or fp32, got {p0.dtype}")
         for i, p in enumerate(parts):
             _dev2d(p, f"parts[{i}]", p0.dtype)
-            if tuple(p.shape) != (m, d) or _ld(p) != ldp:
+            if p.shape != x.shape or _ld(p) != ldp:
                 raise ValueError(f"all parts must be [{m}, {d}] with one row stride")
-            if p.device != x.device:
+            if p.get_device() != index:
                 raise ValueError(f"parts[{i}] is on {p.device}, not on {x.device}")
         h = h_out if h_out is not None else torch.empty((m, d), dtype=x.dtype, device=x.device)
         _dev2d(h, "h_out")
-        if tuple(h.shape) != (m, d) or h.dtype not in _DT:
-            raise ValueError(f"h_out must be [{m}, {d}] bf16 or fp32")
-        a.parts = (_P * len(parts))(*[p.data_ptr() for p in parts])
-        a.num_parts, a.ld_part, a.part_dtype = len(parts), ldp, _DT[p0.dtype]
-        a.h, a.ldh, a.h_dtype = h.data_ptr(), _ld(h), _DT[h.dtype]
+        if h.shape != x.shape or h.dtype not in _DT or h.get_device() != index:
+            raise ValueError(f"h_out must be [{m}, {d}] bf16 or fp32 on {x.device}")
+        num_parts = len(parts)
+        part_array = (_P * num_parts)(*[p.data_ptr() for p in parts])
+        part_dt, h_args = _DT[p0.dtype], (h.data_ptr(), _ld(h), _DT[h.dtype])
     elif h_out is not None:
         raise ValueError("h_out without parts")
+    z_args, z_rows = (0, 0, 0, 0), 0
     if pre_norm == "none":
         if z_out is not None:
             raise ValueError("z_out without pre_norm")
     elif z_dtype == CODES:
-        z = z_out if z_out is not None else _empty_codes(m, d, x.device)
-        codes, scales = z
-        _codes(codes, scales, "z_out", m, -(-d // BLOCK) * BLOCK)
-        _same_device(x, z_codes=codes, z_scales=scales)
-        a.z, a.ldz, a.z_scale, a.ldzs = codes.data_ptr(), _ld(codes), scales.data_ptr(), _lds(scales)
-        a.z_rows = _ROWS[CODES]
+        if z_out is None:
+            codes, scales = z = _empty_codes(m, d, x.device)
+        else:
+            codes, scales = z = z_out
+            _codes(codes, scales, "z_out", m, -(-d // BLOCK) * BLOCK)
+            _same_device(x, z_codes=codes, z_scales=scales)
+        z_args, z_rows = (codes.data_ptr(), _ld(codes), scales.data_ptr(), _lds(scales)), _ROWS[CODES]
     else:
         if z_dtype not in _ROWS:
             raise ValueError("z_dtype must be bf16, fp32 or float8_e4m3fn")
         z = z_out if z_out is not None else torch.empty((m, d), dtype=z_dtype, device=x.device)
         _dev2d(z, "z_out", z_dtype)
-        if tuple(z.shape) != (m, d):
-            raise ValueError(f"z_out must be [{m}, {d}]")
-        a.z, a.ldz, a.z_rows = z.data_ptr(), _ld(z), _ROWS[z_dtype]
-    a.bias = _feature_vec(bias, "bias", x)
-    a.post_weight, a.post_bias = _feature_vec(post_weight, "post_weight", x), _feature_vec(post_bias, "post_bias", x)
-    a.pre_weight, a.pre_bias = _feature_vec(pre_weight, "pre_weight", x), _feature_vec(pre_bias, "pre_bias", x)
-    tables = {}
+        if z.shape != x.shape or z.get_device() != index:
+            raise ValueError(f"z_out must be [{m}, {d}] on {x.device}")
+        z_args, z_rows = (z.data_ptr(), _ld(z), 0, 0), _ROWS[z_dtype]
+    tables, first = [], None
     for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is None:
+            tables.append((0, 0))
             continue
         t = _dev2d(t.unsqueeze(0) if isinstance(t, torch.Tensor) and t.dim() == 1 else t, name)
-        if t.shape[1] != d or t.dtype not in _DT:
-            raise ValueError(f"{name} must be [groups, {d}] bf16 or fp32")
-        tables[name] = t
-        setattr(a, name, t.data_ptr())
-        setattr(a, "ld_" + name, _ld(t))
-    if tables:
-        t0 = next(iter(tables.values()))
-        if any(t.dtype != t0.dtype or t.shape[0] != t0.shape[0] for t in tables.values()):
+        if t.shape[1] != d or t.dtype not in _DT or t.get_device() != index:
+            raise ValueError(f"{name} must be [groups, {d}] bf16 or fp32 on {x.device}")
+        first = t if first is None else first
+        if t.dtype != first.dtype or t.shape[0] != first.shape[0]:
             raise ValueError("gate, scale and shift must have one dtype and one number of groups")
-        a.mod_dtype, a.groups = _DT[t0.dtype], t0.shape[0]
+        tables.append((t.data_ptr(), _ld(t)))
+    groups, mod_dt, index_ptr = 0, 0, 0
+    if first is not None:
+        mod_dt, groups = _DT[first.dtype], first.shape[0]
         if group_index is not None:
             if group_rows is not None:
                 raise ValueError("pass group_rows or group_index, not both")
-            if not group_index.is_cuda or group_index.dtype != torch.int32 or tuple(group_index.shape) != (m,) or \
-                    (m > 1 and group_index.stride(0) != 1):
-                raise ValueError(f"group_index must be a contiguous int32 GPU vector of length {m}")
-            a.group_index = group_index.data_ptr()
-        else:
-            if group_rows is None:
-                if a.groups == 0 or m % a.groups:
-                    raise ValueError(f"{a.groups} groups do not divide {m} rows: pass group_rows or group_index")
-                group_rows = max(1, m // a.groups)
-            a.group_rows = group_rows
+            if group_index.get_device() != index or group_index.dtype != torch.int32 or \
+                    tuple(group_index.shape) != (m,) or (m > 1 and group_index.stride(0) != 1):
+                raise ValueError(f"group_index must be a contiguous int32 vector of length {m} on {x.device}")
+            index_ptr = group_index.data_ptr()
+        elif group_rows is None:
+            if groups == 0 or m % groups:
+                raise ValueError(f"{groups} groups do not divide {m} rows: pass group_rows or group_index")
+            group_rows = max(1, m // groups)
     elif group_index is not None:
         raise ValueError("group_index without a gate, scale or shift")
-    _same_device(x, h_out=h, group_index=group_index, **tables)
-    _call(lib.tp_block_norm, x.device, ctypes.byref(a), _stream(stream, x))
+    (gate_p, gate_ld), (scale_p, scale_ld), (shift_p, shift_ld) = tables
+    args = _PACK.pack(
+        m, d, x.data_ptr(), _ld(x), _DT[x.dtype], part_dt, 0 if part_array is None else ctypes.addressof(part_array),
+        ldp, num_parts, _NORMS[post_norm], _feature_vec(bias, "bias", x), _feature_vec(post_weight, "post_weight", x),
+        _feature_vec(post_bias, "post_bias", x), *h_args, _NORMS[pre_norm], _feature_vec(pre_weight, "pre_weight", x),
+        _feature_vec(pre_bias, "pre_bias", x), *z_args, z_rows, mod_dt, gate_p, scale_p, shift_p, gate_ld, scale_ld,
+        shift_ld, groups, 0 if group_rows is None else group_rows, index_ptr, residual_scale, eps)
+    _call(lib.tp_block_norm, x, stream, args)
     return h, z

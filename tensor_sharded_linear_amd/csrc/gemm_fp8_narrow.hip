@@ -1,4 +1,4 @@
-// gemm_fp8_narrow.hip -- product of quantized rows for few rows (up to 112): split-K, exact products.
+// gemm_fp8_narrow.hip -- product of quantized rows for few rows (up to 96): split-K, exact products.
 //
 // With few rows the weight stream sets the time: 9216 x 6144 codes and their scales are 57 MB, 7 us at
 // 8 TB/s.  So a workgroup of 4 waves owns all M rows, as MB blocks of 16, and a run of output columns
@@ -8,7 +8,7 @@
 //
 //  * Each wave feeds itself: a private LDS ring of D steps, filled by direct-to-LDS loads of whole
 //    128-byte lines (8 lanes a line), D - 1 steps in flight while one is computed, and no barrier.
-//    D fills the 160 KiB of LDS (8 steps for one row block and one column block, 2 for 7 and 2), which
+//    D fills the 160 KiB of LDS (8 steps for one row block and one column block, 2 for 6 and 3), which
 //    holds several times the bytes in flight that the registers of the wave could.
 //  * The fragments are read from LDS as 16-byte chunks (chunk c of row r at c ^ ((r >> 1) & 7)), widened
 //    to bf16 times their scale (exact) and multiplied by v_mfma_f32_16x16x32_bf16: few rows leave the
@@ -77,15 +77,16 @@ __device__ __forceinline__ f32x4 bias4(const uint16_t *b, int n)
     return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
 }
 
-// NB blocks of 16 weight rows cover the workgroup's p.rows output columns (GATED: block 0 the gate
-// rows, block 1 the matching up rows, p.rows <= 16).
+// NB blocks of 16 weight rows cover the workgroup's p.rows output columns (GATED: the first half of the
+// blocks holds gate rows, the second the matching up rows).
 template <int MB, int NB, bool GATED, bool OUT_BF16>
 __global__ __launch_bounds__(kThreadsN) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void gemm_fp8_narrow_kernel(NarrowParams p)
 {
     typedef Ring<MB, NB> R;
     constexpr int D = R::D, kBlocks = R::kBlocks;
-    static_assert(!GATED || NB == 2, "the gated form pairs one gate and one up block");
+    static_assert(!GATED || NB % 2 == 0, "the gated form pairs gate and up blocks");
+    constexpr int kHalf = GATED ? NB / 2 : NB;  // blocks of output columns
     __shared__ __attribute__((aligned(1024))) char lds[R::kBytes];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -94,7 +95,7 @@ void gemm_fp8_narrow_kernel(NarrowParams p)
     char *ring = lds + wave * (D * R::kStep);
     // Row r of block b, W blocks first; rows past the end repeat the last one.
     const auto wrow = [&](int b, int r) {
-        return GATED ? b * p.N + min(n0 + r, n_end - 1) : min(n0 + 16 * b + r, n_end - 1);
+        return GATED ? b / kHalf * p.N + min(n0 + 16 * (b % kHalf) + r, n_end - 1) : min(n0 + 16 * b + r, n_end - 1);
     };
     const auto xrow = [&](int b, int r) { return min(16 * (b - NB) + r, p.M - 1); };
     uint32_t off[kBlocks][2];
@@ -183,7 +184,7 @@ void gemm_fp8_narrow_kernel(NarrowParams p)
     typedef typename std::conditional<OUT_BF16, __bf16, float>::type OutT;
     // Item (block, l): lane l of every wave holds Y[16 m + l % 16][n .. n + 3], n = column base + 16 j +
     // 4 (l / 16); n and n_end are multiples of 4.
-    constexpr int kItems = (GATED ? MB : MB * NB) * 64;
+    constexpr int kItems = MB * kHalf * 64;
     const auto total = [&](int blk, int l) {
         f32x4 v = red[blk * 64 + l];
 #pragma unroll
@@ -192,8 +193,8 @@ void gemm_fp8_narrow_kernel(NarrowParams p)
         return v;
     };
     for (int e = threadIdx.x; e < kItems; e += kThreadsN) {
-        const int l = e & 63, blk = GATED ? (e >> 6) * NB : e >> 6;
-        const int m = 16 * (blk / NB) + (l & 15), n = n0 + 16 * (blk % NB) + 4 * (l >> 4);
+        const int l = e & 63, mb = (e >> 6) / kHalf, jb = (e >> 6) % kHalf, blk = mb * NB + jb;
+        const int m = 16 * mb + (l & 15), n = n0 + 16 * jb + 4 * (l >> 4);
         if (m >= p.M || n >= n_end)
             continue;
         f32x4 v = total(blk, l);
@@ -205,7 +206,7 @@ void gemm_fp8_narrow_kernel(NarrowParams p)
                 v[i] = gelu_tanh(v[i]);
         }
         if (GATED) {
-            f32x4 u = total(blk + 1, l);
+            f32x4 u = total(blk + kHalf, l);
             if (p.bias)
                 u += bias4(p.bias, p.N + n);
 #pragma unroll
@@ -239,15 +240,11 @@ hipError_t launch_nb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
     case 2: return launch_mb<2, NB, GATED>(np, out_bf16, stream);
     case 3: return launch_mb<3, NB, GATED>(np, out_bf16, stream);
     case 4: return launch_mb<4, NB, GATED>(np, out_bf16, stream);
+    case 5: return launch_mb<5, NB, GATED>(np, out_bf16, stream);
     default:
-        if constexpr (NB <= 2) {
-            switch ((np.M + 15) / 16) {
-            case 5: return launch_mb<5, NB, GATED>(np, out_bf16, stream);
-            case 6: return launch_mb<6, NB, GATED>(np, out_bf16, stream);
-            default: return launch_mb<7, NB, GATED>(np, out_bf16, stream);
-            }
-        }
-        return hipErrorInvalidValue;  // pick_rows gives more than 64 rows at most two blocks
+        if constexpr (NB <= 3)
+            return launch_mb<6, NB, GATED>(np, out_bf16, stream);
+        return hipErrorInvalidValue;  // pick_rows gives SwiGLU more than 80 rows at two blocks
     }
 }
 
@@ -257,7 +254,8 @@ hipError_t launch_nb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
 // Ties go to more columns per workgroup.
 int pick_rows(const Fp8Problem &p, int cus)
 {
-    const int max_rows = p.swiglu ? 16 : (p.M > 64 ? 32 : 48);
+    // MB + NB <= 9 blocks fit the ring: three, or with SwiGLU, which pairs them, four up to 80 rows
+    const int max_rows = p.swiglu ? (p.M <= 80 ? 32 : 16) : 48;
     int best = 4;
     double best_cost = -1;
     for (int rows = 4; rows <= max_rows; rows += 4) {
@@ -293,7 +291,7 @@ hipError_t launch_gemm_fp8_narrow(const Fp8Problem &pr, hipStream_t stream)
     np.rows = pick_rows(pr, cu_count());
     np.gelu = pr.gelu;
     if (pr.swiglu)
-        return launch_nb<2, true>(np, pr.out_bf16, stream);
+        return np.rows <= 16 ? launch_nb<2, true>(np, pr.out_bf16, stream) : launch_nb<4, true>(np, pr.out_bf16, stream);
     switch ((np.rows + 15) / 16) {
     case 1: return launch_nb<1, false>(np, pr.out_bf16, stream);
     case 2: return launch_nb<2, false>(np, pr.out_bf16, stream);

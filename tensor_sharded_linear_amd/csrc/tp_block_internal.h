@@ -80,7 +80,7 @@ struct Fp8Problem {
 hipError_t launch_gemm_fp8(const Fp8Problem &p, hipStream_t stream);
 
 // Up to this many rows the kernel for few rows runs.
-constexpr int64_t kFp8NarrowMaxM = 112;
+constexpr int64_t kFp8NarrowMaxM = 96;
 hipError_t launch_gemm_fp8_narrow(const Fp8Problem &p, hipStream_t stream);
 // Four-wave tiles of 32 nxb x 32 nwb; eight-wave tiles of 32 nxb x 128.
 hipError_t launch_gemm_fp8_tiled(const Fp8Problem &p, int nxb, int nwb, hipStream_t stream);
