@@ -95,9 +95,10 @@ def _same_device(x: torch.Tensor, **others: Optional[torch.Tensor]) -> None:
 def _empty_codes(m: int, k: int, device):
     """Codes and scales for m rows of k features; scale rows padded to whole dwords."""
     kb = -(-k // BLOCK)
-    codes = torch.empty((m, kb * BLOCK), dtype=CODES, device=device)
-    scales = torch.empty((m, -(-kb // 4) * 4), dtype=SCALES, device=device)
-    return codes, scales if kb % 4 == 0 else scales[:, :kb]
+    codes = torch.empty_strided((m, kb * BLOCK), (kb * BLOCK, 1), dtype=CODES, device=device)
+    pad = -(-kb // 4) * 4
+    return codes, torch.empty((m, pad), dtype=SCALES, device=device).as_strided((m, kb), (pad, 1)) if kb % 4 else \
+        torch.empty_strided((m, kb), (kb, 1), dtype=SCALES, device=device)
 
 
 def _codes(t: torch.Tensor, s: torch.Tensor, name: str, m: Optional[int] = None, k8: Optional[int] = None) -> None:
@@ -145,12 +146,30 @@ def tp_quantize_fp8(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
     return codes, scales
 
 
-def _operands(x, x_scale, w, w_scale):
-    _codes(x, x_scale, "x")
-    _codes(w, w_scale, "w_shard")
-    if w.shape[1] != x.shape[1]:
-        raise ValueError(f"x is [M, {x.shape[1]}] but w_shard is {tuple(w.shape)}")
-    _same_device(x, x_scale=x_scale, w_shard=w, w_scale=w_scale)
+def _rows(t: torch.Tensor, s: torch.Tensor, name: str):
+    """(rows, features, code row stride, scale row stride) of a (codes, scales) operand."""
+    try:
+        (m, k), (ld, c) = t.shape, t.stride()
+        (ms, kb), (lds, cs) = s.shape, s.stride()
+        good = t.dtype == CODES and s.dtype == SCALES and t.is_cuda and s.is_cuda and c == 1 and ms == m and \
+            kb * BLOCK == k and (cs == 1 or kb == 1)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _codes(t, s, name)   # names what is wrong; what it allows beyond the above is a single column
+        raise ValueError(f"{name} has no columns")
+    return m, k, ld if m > 1 else k, lds if m > 1 else -(-kb // 4) * 4
+
+
+def _operands(x, x_scale, w, w_scale, x_name="x"):
+    m, k, ldx, ldxs = _rows(x, x_scale, x_name)
+    rows, kw, ldw, ldws = _rows(w, w_scale, "w_shard")
+    if kw != k:
+        raise ValueError(f"{x_name} is [M, {k}] but w_shard is {tuple(w.shape)}")
+    index = x.get_device()
+    if not index == x_scale.get_device() == w.get_device() == w_scale.get_device():
+        raise ValueError(f"{x_name}, w_shard and their scales must be on one device")
+    return m, rows, k, (x.data_ptr(), ldx, x_scale.data_ptr(), ldxs, w.data_ptr(), ldw, w_scale.data_ptr(), ldws)
 
 
 def tp_linear_colwise_fp8(x: torch.Tensor, x_scale: torch.Tensor, w_shard: torch.Tensor, w_scale: torch.Tensor,
@@ -162,26 +181,26 @@ def tp_linear_colwise_fp8(x: torch.Tensor, x_scale: torch.Tensor, w_shard: torch
     ``x``/``x_scale`` and ``w_shard``/``w_scale`` as :func:`tp_quantize_fp8` gives them; ``act``,
     ``bias`` and ``out`` as :func:`tp_linear_colwise` (``"swiglu"``: a packed [gate; up] shard)."""
     lib = _library()
-    _operands(x, x_scale, w_shard, w_scale)
+    m, rows, k, operands = _operands(x, x_scale, w_shard, w_scale)
     try:
         a = {"none": _b.TP_ACT_NONE, "gelu_tanh": _b.TP_ACT_GELU_TANH, "swiglu": _b.TP_ACT_SWIGLU}[act]
     except KeyError:
         raise ValueError("act must be 'none', 'gelu_tanh' or 'swiglu'") from None
-    m, k = x.shape
-    rows = w_shard.shape[0]
     if a == _b.TP_ACT_SWIGLU and rows % 2:
         raise ValueError(f"a SwiGLU shard has an even number of rows [gate; up], got {rows}")
     n = rows // 2 if a == _b.TP_ACT_SWIGLU else rows
     bias = _vec(bias, "bias", rows)
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=x.device)
-    out = _dev2d(out, "out")
-    if tuple(out.shape) != (m, n) or out.dtype not in _DT:
-        raise ValueError(f"out must be [{m}, {n}] bf16 or fp32")
+        if out_dtype not in _DT:
+            raise ValueError("out_dtype must be bf16 or fp32")
+        out = torch.empty_strided((m, n), (n, 1), dtype=out_dtype, device=x.device)
+    else:
+        _dev2d(out, "out")
+        if tuple(out.shape) != (m, n) or out.dtype not in _DT:
+            raise ValueError(f"out must be [{m}, {n}] bf16 or fp32")
     _same_device(x, bias=bias, out=out)
-    _call(lib.tp_linear_colwise_fp8, x, stream, x.data_ptr(), _ld(x), x_scale.data_ptr(), _lds(x_scale),
-          w_shard.data_ptr(), _ld(w_shard), w_scale.data_ptr(), _lds(w_scale), _ptr(bias), out.data_ptr(), _ld(out),
-          _DT[out.dtype], a, m, n, k)
+    _call(lib.tp_linear_colwise_fp8, x, stream, *operands, _ptr(bias), out.data_ptr(), _ld(out), _DT[out.dtype], a,
+          m, n, k)
     return out
 
 
@@ -189,18 +208,15 @@ def tp_linear_rowwise_fp8(x_shard: torch.Tensor, x_scale: torch.Tensor, w_shard:
                           w_scale: torch.Tensor, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Rowwise shard of quantized rows: fp32 partial ``out = x_shard @ w_shard.T`` (no bias)."""
     lib = _library()
-    _operands(x_shard, x_scale, w_shard, w_scale)
-    m, k = x_shard.shape
-    n = w_shard.shape[0]
+    m, n, k, operands = _operands(x_shard, x_scale, w_shard, w_scale, "x_shard")
     if out is None:
-        out = torch.empty((m, n), dtype=torch.float32, device=x_shard.device)
-    out = _dev2d(out, "out", torch.float32)
-    if tuple(out.shape) != (m, n):
-        raise ValueError(f"out must be [{m}, {n}]")
-    _same_device(x_shard, out=out)
-    _call(lib.tp_linear_rowwise_fp8, x_shard, stream, x_shard.data_ptr(), _ld(x_shard), x_scale.data_ptr(),
-          _lds(x_scale), w_shard.data_ptr(), _ld(w_shard), w_scale.data_ptr(), _lds(w_scale), out.data_ptr(), _ld(out),
-          m, n, k)
+        out = torch.empty_strided((m, n), (n, 1), dtype=torch.float32, device=x_shard.device)
+    else:
+        _dev2d(out, "out", torch.float32)
+        if tuple(out.shape) != (m, n):
+            raise ValueError(f"out must be [{m}, {n}]")
+        _same_device(x_shard, out=out)
+    _call(lib.tp_linear_rowwise_fp8, x_shard, stream, *operands, out.data_ptr(), _ld(out), m, n, k)
     return out
 
 

@@ -38,90 +38,139 @@ struct NormParams {
     float residual, eps;
 };
 
-// Eight features at column c of a row that starts at element `row` of t.  VEC: rows start at
-// 16-byte addresses, so whole units are one or two 16-byte loads.  Features past D are 0.
-template <bool VEC>
-__device__ __forceinline__ void load8(const void *t, bool f32, int64_t row, int c, int D, float (&v)[8])
+// Rows need only start at an element: the memory system takes wide accesses at any address.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef bf16x8 __attribute__((aligned(2))) bf16x8_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+
+// Eight features as they lie in memory: bf16 in a, fp32 in a and b.  The type is a uniform run-time
+// flag that guards the second load only, so all loads of a row go out before the first is awaited.
+struct Raw {
+    u32x4 a, b;
+};
+
+template <bool TAIL>
+__device__ __forceinline__ Raw load8(const void *t, bool f32, int64_t row, int c, int D)
 {
-    if (VEC && c + 8 <= D) {
-        if (f32) {
-            const f32x4 *s = (const f32x4 *)((const float *)t + row + c);
-            const f32x4 a = s[0], b = s[1];
+    Raw r{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+    if (c + 8 <= D) {
+        const char *p = (const char *)t + (row + c) * (f32 ? 4 : 2);
+        r.a = *(const u32x4_any *)p;
+        if (f32)
+            r.b = *(const u32x4_any *)(p + 16);
+    } else if (TAIL && c < D) {  // D % 8 features, one by one
+        for (int i = 0; i < D - c; ++i) {
+            if (f32) {
+                const uint32_t v = ((const uint32_t *)t)[row + c + i];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = a[i];
-                v[4 + i] = b[i];
-            }
-        } else {
-            const u32x4 a = *(const u32x4 *)((const uint16_t *)t + row + c);
+                for (int k = 0; k < 4; ++k) {
+                    r.a[k] = i == k ? v : r.a[k];
+                    r.b[k] = i == 4 + k ? v : r.b[k];
+                }
+            } else {
+                const uint32_t v = (uint32_t)((const uint16_t *)t)[row + c + i] << (16 * (i & 1));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(a[i] << 16);
-                v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+                for (int k = 0; k < 4; ++k)
+                    r.a[k] |= i / 2 == k ? v : 0;
             }
         }
-        return;
     }
+    return r;
+}
+
+__device__ __forceinline__ void widen(const Raw &r, bool f32, float (&v)[8])
+{
+    if (f32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = 0.f;
-        if (c + i < D)
-            v[i] = f32 ? ((const float *)t)[row + c + i]
-                       : __uint_as_float((uint32_t)((const uint16_t *)t)[row + c + i] << 16);
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(r.a[i]);
+            v[4 + i] = __uint_as_float(r.b[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(r.a[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.a[i] & 0xffff0000u);
+        }
     }
 }
 
-template <bool VEC>
+template <bool TAIL>
 __device__ __forceinline__ void store8(void *t, bool f32, int64_t row, int c, int D, const float (&v)[8])
 {
-    if (VEC && c + 8 <= D) {
+    if (c + 8 <= D) {
         if (f32) {
-            f32x4 *d = (f32x4 *)((float *)t + row + c);
-            d[0] = f32x4{v[0], v[1], v[2], v[3]};
-            d[1] = f32x4{v[4], v[5], v[6], v[7]};
+            float *d = (float *)t + row + c;
+            *(f32x4_any *)d = f32x4{v[0], v[1], v[2], v[3]};
+            *(f32x4_any *)(d + 4) = f32x4{v[4], v[5], v[6], v[7]};
         } else {
             bf16x8 b;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 b[i] = (__bf16)v[i];
-            *(bf16x8 *)((uint16_t *)t + row + c) = b;
+            *(bf16x8_any *)((uint16_t *)t + row + c) = b;
         }
-        return;
-    }
+    } else if (TAIL) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < D) {
-            if (f32)
-                ((float *)t)[row + c + i] = v[i];
-            else
-                ((__bf16 *)t)[row + c + i] = (__bf16)v[i];
-        }
+        for (int i = 0; i < 7; ++i)
+            if (c + i < D) {
+                if (f32)
+                    ((float *)t)[row + c + i] = v[i];
+                else
+                    ((__bf16 *)t)[row + c + i] = (__bf16)v[i];
+            }
+    }
 }
 
-// Sum over the workgroup, the same value in every lane.  `slot` is this call's own LDS row, so
-// one barrier per call suffices.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v)
+{
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+}
+
+// The sum over each row of 16 lanes in its lane 15.
+__device__ __forceinline__ float row_sum(float v)
+{
+    v = dpp_add<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    return dpp_add<0x118, 0xf>(v);
+}
+
+// Sum over the workgroup, the same value in every lane: lanes of a wave by DPP, then the waves (at
+// most 16) through LDS and once more by DPP.  `slot` is this call's own LDS row, so one barrier
+// per call suffices.
 __device__ __forceinline__ float group_sum(float v, float *slot)
 {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1)
-        v += __shfl_xor(v, o, 64);
-    const int waves = blockDim.x >> 6;
+    v = row_sum(v);
+    v = dpp_add<0x142, 0xa>(v);  // row_bcast 15, 31
+    v = dpp_add<0x143, 0xc>(v);
+    const float wave = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+    const int waves = blockDim.x >> 6, lane = threadIdx.x & 63;
     if (waves == 1)
-        return v;
-    if ((threadIdx.x & 63) == 0)
-        slot[threadIdx.x >> 6] = v;
+        return wave;
+    if (lane == 0)
+        slot[threadIdx.x >> 6] = wave;
     __syncthreads();
-    v = slot[0];
-    for (int w = 1; w < waves; ++w)
-        v += slot[w];
-    return v;
+    const float w = row_sum(lane < waves ? slot[lane] : 0.f);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), 15));
 }
 
-template <int U, bool VEC>
+// PRE: the weight and bias are loaded before the sums, so their latency passes beside the reductions.
+template <int U, bool TAIL, bool PRE>
 __device__ __forceinline__ void normalise(float (&v)[U][8], const NormParams &p, int kind, const uint16_t *w,
                                           const uint16_t *b, float *slots)
 {
     const float inv = 1.0f / (float)p.D;
+    Raw rw[U], rb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = 8 * ((int)threadIdx.x + u * (int)blockDim.x);
+        if (PRE && w)
+            rw[u] = load8<TAIL>(w, false, 0, c, p.D);
+        if (PRE && b)
+            rb[u] = load8<TAIL>(b, false, 0, c, p.D);
+    }
     float mean = 0.f;
     if (kind == TP_NORM_LAYER) {
         float s = 0.f;
@@ -138,7 +187,7 @@ __device__ __forceinline__ void normalise(float (&v)[U][8], const NormParams &p,
         const int c = 8 * ((int)threadIdx.x + u * (int)blockDim.x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[u][i] = c + i < p.D ? v[u][i] - mean : 0.f;
+            v[u][i] = c + (TAIL ? i : 0) < p.D ? v[u][i] - mean : 0.f;
             q += v[u][i] * v[u][i];
         }
     }
@@ -151,13 +200,13 @@ __device__ __forceinline__ void normalise(float (&v)[U][8], const NormParams &p,
         for (int i = 0; i < 8; ++i)
             v[u][i] *= r;
         if (w) {
-            load8<VEC>(w, false, 0, c, p.D, g);
+            widen(PRE ? rw[u] : load8<TAIL>(w, false, 0, c, p.D), false, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[u][i] *= g[i];
         }
         if (b) {
-            load8<VEC>(b, false, 0, c, p.D, g);
+            widen(PRE ? rb[u] : load8<TAIL>(b, false, 0, c, p.D), false, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[u][i] += g[i];
@@ -165,79 +214,134 @@ __device__ __forceinline__ void normalise(float (&v)[U][8], const NormParams &p,
     }
 }
 
-template <int U, bool VEC>
-__global__ __launch_bounds__(1024) void block_norm_kernel(NormParams p)
+// One row per workgroup.  NP: the number of parts, or -1 for any.  TAIL: D is no multiple of 8.
+// THREADS: the most that it is launched with.  PRE: everything that a row reads is loaded ahead of its
+// use (not where 16 waves of a long row have 128 registers each).
+template <int U, int NP, bool TAIL, int THREADS, bool PRE>
+__global__ __launch_bounds__(THREADS) void block_norm_kernel(NormParams p)
 {
     __shared__ float slots[4 * kMaxWaves];
     const int64_t row = p.row0 + blockIdx.x;
+    const int parts = NP >= 0 ? NP : p.num_parts;
     const int64_t group = p.index ? (int64_t)p.index[row] : row / p.group_rows;
     const bool modulated = group >= 0 && group < p.groups;
+    const auto col = [&](int u) { return 8 * ((int)threadIdx.x + u * (int)blockDim.x); };
     float h[U][8], t[8];
+    Raw rx[U];
+    if (PRE || NP == 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        load8<VEC>(p.x, p.x_f32, row * p.ldx, 8 * ((int)threadIdx.x + u * (int)blockDim.x), p.D, h[u]);
-    if (p.num_parts) {
+        for (int u = 0; u < U; ++u)
+            rx[u] = load8<TAIL>(p.x, p.x_f32, row * p.ldx, col(u), p.D);
+    }
+    if (NP != 0) {
         float y[U][8];
+        constexpr int kAtOnce = NP > 0 ? NP : 1;
+        Raw rp[kAtOnce][U];
+        Raw rbias[U], rgate[U];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                rp[q][u] = load8<TAIL>(p.parts[q], p.part_f32, row * p.ld_part, col(u), p.D);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = 8 * ((int)threadIdx.x + u * (int)blockDim.x);
-            load8<VEC>(p.parts[0], p.part_f32, row * p.ld_part, c, p.D, y[u]);
-            for (int q = 1; q < p.num_parts; ++q) {
-                load8<VEC>(p.parts[q], p.part_f32, row * p.ld_part, c, p.D, t);
+            if (PRE && p.bias)
+                rbias[u] = load8<TAIL>(p.bias, false, 0, col(u), p.D);
+            if (PRE && p.gate && modulated)
+                rgate[u] = load8<TAIL>(p.gate, p.mod_f32, group * p.ld_gate, col(u), p.D);
+        }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[u][i] += t[i];
+        for (int u = 0; u < U; ++u)
+            widen(rp[0][u], p.part_f32, y[u]);
+        if (NP > 0) {
+#pragma unroll
+            for (int q = 1; q < kAtOnce; ++q)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    widen(rp[q][u], p.part_f32, t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        y[u][i] += t[i];
+                }
+        } else {
+            for (int q = 1; q < parts; ++q) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    rp[0][u] = load8<TAIL>(p.parts[q], p.part_f32, row * p.ld_part, col(u), p.D);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    widen(rp[0][u], p.part_f32, t);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        y[u][i] += t[i];
+                }
             }
-            if (p.bias) {
-                load8<VEC>(p.bias, false, 0, c, p.D, t);
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                widen(PRE ? rbias[u] : load8<TAIL>(p.bias, false, 0, col(u), p.D), false, t);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     y[u][i] += t[i];
             }
         }
         if (p.post != TP_NORM_NONE)
-            normalise<U, VEC>(y, p, p.post, p.post_w, p.post_b, slots);
+            normalise<U, TAIL, PRE>(y, p, p.post, p.post_w, p.post_b, slots);
+        const bool branch = !p.gate || modulated;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = 8 * ((int)threadIdx.x + u * (int)blockDim.x);
             if (p.gate && modulated) {
-                load8<VEC>(p.gate, p.mod_f32, group * p.ld_gate, c, p.D, t);
+                widen(PRE ? rgate[u] : load8<TAIL>(p.gate, p.mod_f32, group * p.ld_gate, col(u), p.D), p.mod_f32, t);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     y[u][i] *= t[i];
             }
-            const bool branch = !p.gate || modulated;
+            widen(PRE ? rx[u] : load8<TAIL>(p.x, p.x_f32, row * p.ldx, col(u), p.D), p.x_f32, h[u]);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 h[u][i] = p.residual * h[u][i] + (branch ? y[u][i] : 0.f);
-            store8<VEC>(p.h, p.h_f32, row * p.ldh, c, p.D, h[u]);
+            store8<TAIL>(p.h, p.h_f32, row * p.ldh, col(u), p.D, h[u]);
         }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            widen(rx[u], p.x_f32, h[u]);
     }
     if (p.pre == TP_NORM_NONE)
         return;
-    normalise<U, VEC>(h, p, p.pre, p.pre_w, p.pre_b, slots + 2 * kMaxWaves);
+    const bool scaled = p.scale && modulated, shifted = p.shift && modulated;
+    Raw rs[U], rt[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int c = 8 * ((int)threadIdx.x + u * (int)blockDim.x);
-        if (p.scale && modulated) {
-            load8<VEC>(p.scale, p.mod_f32, group * p.ld_scale, c, p.D, t);
+        if (PRE && scaled)
+            rs[u] = load8<TAIL>(p.scale, p.mod_f32, group * p.ld_scale, col(u), p.D);
+        if (PRE && shifted)
+            rt[u] = load8<TAIL>(p.shift, p.mod_f32, group * p.ld_shift, col(u), p.D);
+    }
+    normalise<U, TAIL, PRE>(h, p, p.pre, p.pre_w, p.pre_b, slots + 2 * kMaxWaves);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int c = col(u);
+        if (scaled) {
+            widen(PRE ? rs[u] : load8<TAIL>(p.scale, p.mod_f32, group * p.ld_scale, c, p.D), p.mod_f32, t);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 h[u][i] *= 1.0f + t[i];
         }
-        if (p.shift && modulated) {
-            load8<VEC>(p.shift, p.mod_f32, group * p.ld_shift, c, p.D, t);
+        if (shifted) {
+            widen(PRE ? rt[u] : load8<TAIL>(p.shift, p.mod_f32, group * p.ld_shift, c, p.D), p.mod_f32, t);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 h[u][i] += t[i];
         }
         if (p.z_rows != TP_ROWS_FP8) {
-            store8<VEC>(p.z, p.z_rows == TP_ROWS_F32, row * p.ldz, c, p.D, h[u]);
+            store8<TAIL>(p.z, p.z_rows == TP_ROWS_F32, row * p.ldz, c, p.D, h[u]);
         } else {
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                h[u][i] = c + i < p.D ? h[u][i] : 0.f;
+                h[u][i] = c + (TAIL ? i : 0) < p.D ? h[u][i] : 0.f;
                 m = max(m, __float_as_uint(h[u][i]) & 0x7fffffffu);
             }
             const int s = scale_byte(row16_max(m));
@@ -254,17 +358,30 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(NormParams p)
 // into further launches.
 constexpr int64_t kRowsPerLaunch = (int64_t)1 << 21;
 
-template <int U>
-void launch_u(NormParams p, int64_t M, bool vec, int waves, hipStream_t stream)
+typedef void (*NormKernel)(NormParams);
+
+// Up to 4 waves a row, or one unit a lane: everything ahead; the common part counts unrolled.
+template <int U, int THREADS>
+NormKernel eager_kernel(int parts, bool tail)
 {
-    const dim3 block(64 * waves);
-    for (p.row0 = 0; p.row0 < M; p.row0 += kRowsPerLaunch) {
-        const dim3 grid((unsigned)(M - p.row0 < kRowsPerLaunch ? M - p.row0 : kRowsPerLaunch));
-        if (vec)
-            hipLaunchKernelGGL((block_norm_kernel<U, true>), grid, block, 0, stream, p);
-        else
-            hipLaunchKernelGGL((block_norm_kernel<U, false>), grid, block, 0, stream, p);
+    if (tail)
+        return parts == 0 ? block_norm_kernel<U, 0, true, THREADS, true> : block_norm_kernel<U, -1, true, THREADS, true>;
+    switch (parts) {
+    case 0: return block_norm_kernel<U, 0, false, THREADS, true>;
+    case 1: return block_norm_kernel<U, 1, false, THREADS, true>;
+    case 2: return block_norm_kernel<U, 2, false, THREADS, true>;
+    case 4: return block_norm_kernel<U, 4, false, THREADS, true>;
+    default: return block_norm_kernel<U, -1, false, THREADS, true>;
     }
+}
+
+// Longer rows: more than 4 waves of two to four units a lane.
+template <int U>
+NormKernel lean_kernel(int parts, bool tail)
+{
+    if (tail)
+        return parts == 0 ? block_norm_kernel<U, 0, true, 1024, false> : block_norm_kernel<U, -1, true, 1024, false>;
+    return parts == 0 ? block_norm_kernel<U, 0, false, 1024, false> : block_norm_kernel<U, -1, false, 1024, false>;
 }
 
 }  // namespace
@@ -276,28 +393,8 @@ hipError_t launch_block_norm(const tp_block_norm_args &a, hipStream_t stream)
     p.D8 = a.z_rows == TP_ROWS_FP8 && a.z ? (int)((a.D + kQBlock - 1) / kQBlock * kQBlock) : p.D;
     p.x = a.x;
     p.num_parts = a.num_parts;
-    bool vec = true;
-    const auto rows = [&](const void *t, int64_t ld, int es) {
-        vec = vec && (uintptr_t)t % 16 == 0 && ld * es % 16 == 0;
-    };
-    for (int i = 0; i < a.num_parts; ++i) {
+    for (int i = 0; i < a.num_parts; ++i)
         p.parts[i] = a.parts[i];
-        rows(a.parts[i], a.ld_part, a.part_dtype == TP_F32 ? 4 : 2);
-    }
-    rows(a.x, a.ldx, a.x_dtype == TP_F32 ? 4 : 2);
-    for (const void *v : {a.bias, a.post_weight, a.post_bias, a.pre_weight, a.pre_bias})
-        rows(v, 0, 2);
-    if (a.num_parts)
-        rows(a.h, a.ldh, a.h_dtype == TP_F32 ? 4 : 2);
-    if (a.z && a.z_rows != TP_ROWS_FP8)
-        rows(a.z, a.ldz, a.z_rows == TP_ROWS_F32 ? 4 : 2);
-    const int ms = a.mod_dtype == TP_F32 ? 4 : 2;
-    if (a.gate)
-        rows(a.gate, a.ld_gate, ms);
-    if (a.scale)
-        rows(a.scale, a.ld_scale, ms);
-    if (a.shift)
-        rows(a.shift, a.ld_shift, ms);
     p.bias = (const uint16_t *)a.bias;
     p.post_w = (const uint16_t *)a.post_weight;
     p.post_b = (const uint16_t *)a.post_bias;
@@ -329,16 +426,32 @@ hipError_t launch_block_norm(const tp_block_norm_args &a, hipStream_t stream)
     p.mod_f32 = a.mod_dtype == TP_F32;
     p.residual = a.residual_scale;
     p.eps = a.eps;
-    // Units of 8 features per row; the fewest waves that hold a row in at most 4 units a lane.
+    // Units of 8 features per row and lane, and waves per row.  Few rows: as many waves as there are
+    // units, for the latency of one row; many rows: three or four units a lane, whichever leaves
+    // fewer lanes idle.
     const int units = (p.D8 + 7) / 8;
-    int waves = 1;
-    while (waves < kMaxWaves && units > 4 * 64 * waves)
-        waves *= 2;
-    switch ((units + 64 * waves - 1) / (64 * waves)) {
-    case 1: launch_u<1>(p, a.M, vec, waves, stream); break;
-    case 2: launch_u<2>(p, a.M, vec, waves, stream); break;
-    case 3: launch_u<3>(p, a.M, vec, waves, stream); break;
-    default: launch_u<4>(p, a.M, vec, waves, stream); break;
+    const auto waves_of = [&](int u) { return (units + 64 * u - 1) / (64 * u); };
+    int u = a.M <= cu_count() ? 1 : (waves_of(3) * 3 <= waves_of(4) * 4 ? 3 : 4);
+    while (waves_of(u) > kMaxWaves)
+        ++u;
+    const int waves = waves_of(u);
+    while (u > 1 && waves_of(u - 1) == waves)
+        --u;
+    const bool tail = p.D % 8 != 0;
+    NormKernel kernel;
+    if (waves <= 4)
+        kernel = u == 1   ? eager_kernel<1, 256>(p.num_parts, tail)
+                 : u == 2 ? eager_kernel<2, 256>(p.num_parts, tail)
+                 : u == 3 ? eager_kernel<3, 256>(p.num_parts, tail)
+                          : eager_kernel<4, 256>(p.num_parts, tail);
+    else
+        kernel = u == 1   ? eager_kernel<1, 1024>(p.num_parts, tail)
+                 : u == 2 ? lean_kernel<2>(p.num_parts, tail)
+                 : u == 3 ? lean_kernel<3>(p.num_parts, tail)
+                          : lean_kernel<4>(p.num_parts, tail);
+    for (p.row0 = 0; p.row0 < a.M; p.row0 += kRowsPerLaunch) {
+        const dim3 grid((unsigned)(a.M - p.row0 < kRowsPerLaunch ? a.M - p.row0 : kRowsPerLaunch));
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, stream, p);
     }
     return hipGetLastError();
 }

@@ -13,13 +13,15 @@ namespace tpl {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+// Rows need only start at an element: the memory system takes wide accesses at any address.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
 constexpr int kThreads = 256;
 constexpr int kUnits = kThreads / 16;  // blocks per workgroup and step
 
 __device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
-template <bool F32, bool VEC>
+template <bool F32>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantProblem p, int kb, int64_t wg0, int64_t units)
 {
     const int64_t first = (wg0 + blockIdx.x) * kUnits;  // uniform
@@ -32,17 +34,17 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(QuantProblem p, int 
         return;  // whole 16-lane groups
     const int64_t k = (int64_t)blk * kQBlock + 8 * (threadIdx.x & 15);
     float v[8];
-    if (VEC && k + 8 <= p.K) {
+    if (k + 8 <= p.K) {
         if (F32) {
             const float *src = (const float *)p.x + row * p.ldx + k;
-            const u32x4 a = *(const u32x4 *)src, b = *(const u32x4 *)(src + 4);
+            const u32x4 a = *(const u32x4_any *)src, b = *(const u32x4_any *)(src + 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[i] = __uint_as_float(a[i]);
                 v[4 + i] = __uint_as_float(b[i]);
             }
         } else {
-            const u32x4 a = *(const u32x4 *)((const uint16_t *)p.x + row * p.ldx + k);
+            const u32x4 a = *(const u32x4_any *)((const uint16_t *)p.x + row * p.ldx + k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[2 * i] = __uint_as_float(a[i] << 16);
@@ -75,10 +77,7 @@ hipError_t launch_quantize(const QuantProblem &p, hipStream_t stream)
     const int kb = (int)((p.K + kQBlock - 1) / kQBlock);
     const int64_t units = p.M * kb;
     const int64_t wgs = (units + kUnits - 1) / kUnits;
-    const int es = p.x_f32 ? 4 : 2;
-    const bool vec = (uintptr_t)p.x % 16 == 0 && p.ldx * es % 16 == 0;
-    const auto kernel = p.x_f32 ? (vec ? quantize_kernel<true, true> : quantize_kernel<true, false>)
-                                : (vec ? quantize_kernel<false, true> : quantize_kernel<false, false>);
+    const auto kernel = p.x_f32 ? quantize_kernel<true> : quantize_kernel<false>;
     // A launch holds fewer than 2^32 threads; more blocks go into further launches.
     constexpr int64_t kPerLaunch = (int64_t)1 << 23;
     for (int64_t wg0 = 0; wg0 < wgs; wg0 += kPerLaunch) {
