@@ -220,12 +220,11 @@ def tp_linear_rowwise_fp8(x_shard: torch.Tensor, x_scale: torch.Tensor, w_shard:
     return out
 
 
-def _feature_vec(t: Optional[torch.Tensor], name: str, x: torch.Tensor) -> int:
+def _feature_vec(t: Optional[torch.Tensor], name: str, d: int, index: int) -> int:
     if t is None:
         return 0
-    _vec(t, name, x.shape[1])
-    if t.get_device() != x.get_device():
-        raise ValueError(f"{name} is on {t.device}, not on {x.device}")
+    if t.get_device() != index or t.dtype != torch.bfloat16 or t.shape != (d,) or (d > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous bf16 vector of length {d} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -271,16 +270,17 @@ def tp_block_norm(x: torch.Tensor, parts: Optional[Sequence[torch.Tensor]] = Non
         ldp = _ld(p0)
         if p0.dtype not in _DT:
             raise TypeError(f"parts must be bf16 or fp32, got {p0.dtype}")
+        strides = p0.stride()
         for i, p in enumerate(parts):
-            _dev2d(p, f"parts[{i}]", p0.dtype)
-            if p.shape != x.shape or _ld(p) != ldp:
-                raise ValueError(f"all parts must be [{m}, {d}] with one row stride")
-            if p.get_device() != index:
-                raise ValueError(f"parts[{i}] is on {p.device}, not on {x.device}")
-        h = h_out if h_out is not None else torch.empty((m, d), dtype=x.dtype, device=x.device)
-        _dev2d(h, "h_out")
-        if h.shape != x.shape or h.dtype not in _DT or h.get_device() != index:
-            raise ValueError(f"h_out must be [{m}, {d}] bf16 or fp32 on {x.device}")
+            if p.shape != x.shape or p.dtype != p0.dtype or p.get_device() != index or \
+                    (p.stride() != strides and _ld(_dev2d(p, f"parts[{i}]")) != ldp):
+                raise ValueError(f"all parts must be [{m}, {d}], of one dtype and row stride, on {x.device}")
+        if h_out is None:
+            h = torch.empty_strided((m, d), (d, 1), dtype=x.dtype, device=x.device)
+        else:
+            h = _dev2d(h_out, "h_out")
+            if h.shape != x.shape or h.dtype not in _DT or h.get_device() != index:
+                raise ValueError(f"h_out must be [{m}, {d}] bf16 or fp32 on {x.device}")
         num_parts = len(parts)
         part_array = (_P * num_parts)(*[p.data_ptr() for p in parts])
         part_dt, h_args = _DT[p0.dtype], (h.data_ptr(), _ld(h), _DT[h.dtype])
@@ -301,19 +301,23 @@ def tp_block_norm(x: torch.Tensor, parts: Optional[Sequence[torch.Tensor]] = Non
     else:
         if z_dtype not in _ROWS:
             raise ValueError("z_dtype must be bf16, fp32 or float8_e4m3fn")
-        z = z_out if z_out is not None else torch.empty((m, d), dtype=z_dtype, device=x.device)
-        _dev2d(z, "z_out", z_dtype)
-        if z.shape != x.shape or z.get_device() != index:
-            raise ValueError(f"z_out must be [{m}, {d}] on {x.device}")
+        if z_out is None:
+            z = torch.empty_strided((m, d), (d, 1), dtype=z_dtype, device=x.device)
+        else:
+            z = _dev2d(z_out, "z_out", z_dtype)
+            if z.shape != x.shape or z.get_device() != index:
+                raise ValueError(f"z_out must be [{m}, {d}] on {x.device}")
         z_args, z_rows = (z.data_ptr(), _ld(z), 0, 0), _ROWS[z_dtype]
     tables, first = [], None
     for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is None:
             tables.append((0, 0))
             continue
-        t = _dev2d(t.unsqueeze(0) if isinstance(t, torch.Tensor) and t.dim() == 1 else t, name)
-        if t.shape[1] != d or t.dtype not in _DT or t.get_device() != index:
-            raise ValueError(f"{name} must be [groups, {d}] bf16 or fp32 on {x.device}")
+        if t.dim() == 1:
+            t = t.unsqueeze(0)
+        if t.dim() != 2 or t.shape[1] != d or t.dtype not in _DT or t.get_device() != index or \
+                (d > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name} must be [groups, {d}] bf16 or fp32 on {x.device}, with unit column stride")
         first = t if first is None else first
         if t.dtype != first.dtype or t.shape[0] != first.shape[0]:
             raise ValueError("gate, scale and shift must have one dtype and one number of groups")
@@ -337,9 +341,9 @@ def tp_block_norm(x: torch.Tensor, parts: Optional[Sequence[torch.Tensor]] = Non
     (gate_p, gate_ld), (scale_p, scale_ld), (shift_p, shift_ld) = tables
     args = _PACK.pack(
         m, d, x.data_ptr(), _ld(x), _DT[x.dtype], part_dt, 0 if part_array is None else ctypes.addressof(part_array),
-        ldp, num_parts, _NORMS[post_norm], _feature_vec(bias, "bias", x), _feature_vec(post_weight, "post_weight", x),
-        _feature_vec(post_bias, "post_bias", x), *h_args, _NORMS[pre_norm], _feature_vec(pre_weight, "pre_weight", x),
-        _feature_vec(pre_bias, "pre_bias", x), *z_args, z_rows, mod_dt, gate_p, scale_p, shift_p, gate_ld, scale_ld,
+        ldp, num_parts, _NORMS[post_norm], _feature_vec(bias, "bias", d, index), _feature_vec(post_weight, "post_weight", d, index),
+        _feature_vec(post_bias, "post_bias", d, index), *h_args, _NORMS[pre_norm], _feature_vec(pre_weight, "pre_weight", d, index),
+        _feature_vec(pre_bias, "pre_bias", d, index), *z_args, z_rows, mod_dt, gate_p, scale_p, shift_p, gate_ld, scale_ld,
         shift_ld, groups, 0 if group_rows is None else group_rows, index_ptr, residual_scale, eps)
     _call(lib.tp_block_norm, x, stream, args)
     return h, z

@@ -167,7 +167,7 @@ void gemm_fp8_small_kernel(SmallParams p)
     f32x4 acc[NXB][NWB];
     zero<NXB, NWB>(acc);
     mainloop_small<NXB, NWB, kGated>(p, lds, c, tm * L::BM, tn * kTileCols, acc);
-    epilogue<NXB, NWB, OUT_BF16, HAS_BIAS, ACT>(p, reinterpret_cast<uint16_t *>(lds), c, tm * L::BM, tn * kTileCols, acc);
+    epilogue<NXB, NWB, OUT_BF16, HAS_BIAS, ACT, true>(p, reinterpret_cast<uint16_t *>(lds), c, tm * L::BM, tn * kTileCols, acc);
 }
 
 template <int NXB, int NWB, bool OUT_BF16, bool HAS_BIAS, int ACT>

@@ -471,7 +471,7 @@ void gemm_fp8_nt_kernel(Fp8Params p)
     else
         mainloop8<NXB, NWB, kGated>(p, lds, c, tm * BM, tn * kTileCols, acc);
     finish<NXB, NWB>(acc);
-    epilogue<NXB, NWB, !EXACT, HAS_BIAS, ACT>(p, reinterpret_cast<uint16_t *>(lds), c, tm * BM, tn * kTileCols, acc);
+    epilogue<NXB, NWB, !EXACT, HAS_BIAS, ACT, true>(p, reinterpret_cast<uint16_t *>(lds), c, tm * BM, tn * kTileCols, acc);
 }
 
 template <int NXB, int NWB, bool EXACT, bool HAS_BIAS, int ACT>

@@ -135,7 +135,7 @@ constexpr int kActSwiglu = 2;  // W tile = interleaved [gate; up] 64-row blocks,
 // output columns, or 8 NWB with SwiGLU: there its blocks j < NWB / 2 hold the gate
 // and j >= NWB / 2 the up projection of the same columns, and the output is
 // silu(gate + b_gate) * (up + b_up), the bias being [b_gate; b_up] (2 N).
-template <int NXB, int NWB, bool OUT_BF16, bool HAS_BIAS, int ACT, typename Params>
+template <int NXB, int NWB, bool OUT_BF16, bool HAS_BIAS, int ACT, bool BIAS_AHEAD = false, typename Params>
 __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const Ctx &c, int m0, int n0,
                                          const f32x4 (&acc)[NXB][NWB])
 {
@@ -160,6 +160,26 @@ __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const C
         const bf16x4 bb = *reinterpret_cast<const bf16x4 *>(p.bias + e);
         return f32x4{(float)bb[0], (float)bb[1], (float)bb[2], (float)bb[3]};
     };
+    // BIAS_AHEAD: the wave's bias values in registers before the first slice.  Loaded where they are
+    // used, each slice waits for them again, as the output's stores might change them.
+    bf16x4 bias_v[kGated ? 2 : 1][JO];
+    if constexpr (HAS_BIAS && BIAS_AHEAD) {
+#pragma unroll
+        for (int j = 0; j < JO; ++j) {
+            const int n = min(n0 + c.wave_n * WNO + j * 16 + ncol, p.N - 4);
+            bias_v[0][j] = *reinterpret_cast<const bf16x4 *>(p.bias + n);
+            if constexpr (kGated)
+                bias_v[1][j] = *reinterpret_cast<const bf16x4 *>(p.bias + p.N + n);
+        }
+    }
+    auto bias_of = [&](int up, int j, int n) {
+        if constexpr (BIAS_AHEAD) {
+            const bf16x4 bb = bias_v[up][j];
+            return f32x4{(float)bb[0], (float)bb[1], (float)bb[2], (float)bb[3]};
+        } else {
+            return bias4(up * p.N + n);
+        }
+    };
     constexpr int kVec = 16 / kOutEs;              // elements per 16-byte vector
     constexpr int kVecPerRow = WNO / kVec;
     // When a pass of 64 lanes covers whole rows, each lane keeps its row and column for
@@ -177,7 +197,7 @@ __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const C
             const int n = n0 + c.wave_n * WNO + j * 16 + ncol;  // N % 16 == 0: n < N covers n + 3
             f32x4 v = acc[i][j];
             if (HAS_BIAS && n < p.N)
-                v = v + bias4(n);
+                v = v + bias_of(0, j, n);
             if (ACT == kActGelu) {
                 v[0] = gelu_tanh(v[0]);
                 v[1] = gelu_tanh(v[1]);
@@ -187,7 +207,7 @@ __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const C
             if (kGated) {
                 f32x4 u = acc[i][j + NWB / 2];
                 if (HAS_BIAS && n < p.N)
-                    u = u + bias4(p.N + n);
+                    u = u + bias_of(1, j, n);
                 v[0] = silu(v[0]) * u[0];
                 v[1] = silu(v[1]) * u[1];
                 v[2] = silu(v[2]) * u[2];
