@@ -60,7 +60,7 @@ __device__ __forceinline__ void mainloop_small(const SmallParams &p, char *lds, 
     typedef STile<NXB, NWB> L;
     constexpr int BM = L::BM, BN = L::BN, S = L::kStages;
     constexpr int kDmaX = BM / 64, kDmaW = BN / 64, kPer = kDmaX + kDmaW;
-    static_assert(S >= 2 && (S - 2) * kPer <= 60, "the wait count fits vmcnt");
+    static_assert(S >= 2 && (S - 1) * kPer <= 60, "the wait count fits vmcnt");
     // weight row of a tile row; gated: a wave column's first half holds gate rows, its second up rows
     auto wrow = [&](int r) {
         if (!GATED)
@@ -95,56 +95,90 @@ __device__ __forceinline__ void mainloop_small(const SmallParams &p, char *lds, 
     };
     issue_scales(0);
 #pragma unroll
-    for (int u = 0; u < S - 1; ++u)
+    for (int u = 0; u < S; ++u)
         issue(u, u);
     const int fr = c.lane & 15, g = c.lane >> 4, swz = (c.lane >> 1) & 7;
     const int xrow = c.wave_m * L::WM + fr, wr0 = c.wave_n * L::WN + fr;
-    int stage = 0;
-    for (int t = 0; t < T; ++t) {
-        // k-tile t has landed (the S - 2 k-tiles after it stay in flight), and k-tile t - 1 has been
-        // read by every wave, so its stage takes k-tile t + S - 1.  The scales of a group are
-        // issued at its predecessor's first k-tile: at least three k-tiles of loads later they
-        // are behind every wait that leaves at most S - 2 <= 3 k-tiles in flight.
-        wait_dma_keep<(S - 2) * kPer>();
-        barrier_only();
-        issue(t + S - 1, stage == 0 ? S - 1 : stage - 1);
-        if ((t & 3) == 0)
-            issue_scales((t >> 2) + 1);
+    // A k-tile's codes and scales in registers, read one k-tile ahead of the products that use them.
+    struct Codes {
+        i32x4 x[2][NXB], w[2][NWB];
+        uint32_t sx[NXB], sw[NWB];
+    };
+    auto read = [&](int u, int stage, Codes &r) {
         const char *xs = lds + stage * L::kStageBytes, *ws = xs + BM * kRow;
-        const char *sc = sl + ((t >> 2) & 1) * 2048;
-        float sx[NXB], sw[NWB];
+        const char *sc = sl + ((u >> 2) & 1) * 2048;
 #pragma unroll
         for (int i = 0; i < NXB; ++i)
-            sx[i] = factor(*reinterpret_cast<const uint32_t *>(sc + (xrow + 16 * i) * 4), t);
+            r.sx[i] = *reinterpret_cast<const uint32_t *>(sc + (xrow + 16 * i) * 4);
 #pragma unroll
         for (int j = 0; j < NWB; ++j)
-            sw[j] = factor(*reinterpret_cast<const uint32_t *>(sc + (BM + wr0 + 16 * j) * 4), t);
+            r.sw[j] = *reinterpret_cast<const uint32_t *>(sc + (BM + wr0 + 16 * j) * 4);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int cpos = ((4 * h + g) ^ swz) * 16;
-            i32x4 rx[NXB], rw[NWB];
 #pragma unroll
             for (int j = 0; j < NWB; ++j)
-                rw[j] = *reinterpret_cast<const i32x4 *>(ws + (wr0 + 16 * j) * kRow + cpos);
+                r.w[h][j] = *reinterpret_cast<const i32x4 *>(ws + (wr0 + 16 * j) * kRow + cpos);
 #pragma unroll
             for (int i = 0; i < NXB; ++i)
-                rx[i] = *reinterpret_cast<const i32x4 *>(xs + (xrow + 16 * i) * kRow + cpos);
+                r.x[h][i] = *reinterpret_cast<const i32x4 *>(xs + (xrow + 16 * i) * kRow + cpos);
+        }
+    };
+    auto multiply = [&](int u, const Codes &r) {
+        float fx[NXB], fw[NWB];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                bf16x8 fw[NWB];
+        for (int i = 0; i < NXB; ++i)
+            fx[i] = factor(r.sx[i], u);
+#pragma unroll
+        for (int j = 0; j < NWB; ++j)
+            fw[j] = factor(r.sw[j], u);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            bf16x8 w[NWB];
+#pragma unroll
+            for (int j = 0; j < NWB; ++j)
+                w[j] = widen8(r.w[s / 2][j][s % 2 * 2], r.w[s / 2][j][s % 2 * 2 + 1], fw[j]);
+#pragma unroll
+            for (int i = 0; i < NXB; ++i) {
+                const bf16x8 x = widen8(r.x[s / 2][i][s % 2 * 2], r.x[s / 2][i][s % 2 * 2 + 1], fx[i]);
 #pragma unroll
                 for (int j = 0; j < NWB; ++j)
-                    fw[j] = widen8(rw[j][2 * s], rw[j][2 * s + 1], sw[j]);
-#pragma unroll
-                for (int i = 0; i < NXB; ++i) {
-                    const bf16x8 fx = widen8(rx[i][2 * s], rx[i][2 * s + 1], sx[i]);
-#pragma unroll
-                    for (int j = 0; j < NWB; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[j], fx, acc[i][j], 0, 0, 0);
-                }
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j], x, acc[i][j], 0, 0, 0);
             }
         }
-        stage = stage == S - 1 ? 0 : stage + 1;
+    };
+    // k-tile u is in stage u % S.
+    wait_dma_keep<(S - 1) * kPer>();
+    barrier_only();
+    Codes ca, cb;
+    read(0, 0, ca);
+    int stage = 0;  // of k-tile t
+    // At the barrier of k-tile t, k-tile t + 1 has landed (the S - 2 after it stay in flight) and every
+    // wave has k-tile t in registers, so its stage takes k-tile t + S.  The scales of the next group
+    // of four k-tiles go out at a group's first k-tile, ahead of its loads, and are read three
+    // k-tiles later, behind a wait that leaves at most S - 2 <= 3 k-tiles of loads in flight.
+    auto body = [&](int t, const Codes &cur, Codes &nxt) {
+        const int next = stage == S - 1 ? 0 : stage + 1;
+        wait_dma_keep<(S - 2) * kPer>();
+        barrier_only();
+        if ((t & 3) == 0)
+            issue_scales((t >> 2) + 1);
+        issue(t + S, stage);
+        // lgkmcnt(0) once more, in a form that the compiler sees: without it, it takes `cur` for still
+        // on its way and waits for the reads below before the products
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        read(t + 1, next, nxt);
+        __builtin_amdgcn_sched_barrier(0);  // the reads go out before the products, not after them
+        multiply(t, cur);
+        stage = next;
+    };
+    for (int t = 0;;) {
+        body(t, ca, cb);
+        if (++t == T)
+            break;
+        body(t, cb, ca);
+        if (++t == T)
+            break;
     }
     wait_dma();  // the repeated loads of the last k-tile, before the epilogue reuses the LDS
 }
