@@ -53,7 +53,10 @@ __device__ __forceinline__ void dma_to_lds4(const char *src, char *dst)
     __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 4, 0, 0);
 }
 
-template <int NXB, int NWB, bool GATED>
+__device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+
+// EXACT: products of the codes widened to bf16; otherwise on the 8-bit matrix cores.
+template <int NXB, int NWB, bool GATED, bool EXACT>
 __device__ __forceinline__ void mainloop_small(const SmallParams &p, char *lds, const Ctx &c, int m0, int n0,
                                                f32x4 (&acc)[NXB][NWB])
 {
@@ -125,6 +128,17 @@ __device__ __forceinline__ void mainloop_small(const SmallParams &p, char *lds, 
         }
     };
     auto multiply = [&](int u, const Codes &r) {
+        if constexpr (!EXACT) {
+            const int byte = 8 * (u & 3);
+#pragma unroll
+            for (int i = 0; i < NXB; ++i)
+#pragma unroll
+                for (int j = 0; j < NWB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        join(r.w[0][j], r.w[1][j]), join(r.x[0][i], r.x[1][i]), acc[i][j], 0, 0, 0, r.sw[j] >> byte, 0,
+                        r.sx[i] >> byte);
+            return;
+        }
         float fx[NXB], fw[NWB];
 #pragma unroll
         for (int i = 0; i < NXB; ++i)
@@ -200,7 +214,7 @@ void gemm_fp8_small_kernel(SmallParams p)
     tile_of(xcd_contiguous(blockIdx.x, p.tiles_m * p.tiles_n), p, tm, tn);
     f32x4 acc[NXB][NWB];
     zero<NXB, NWB>(acc);
-    mainloop_small<NXB, NWB, kGated>(p, lds, c, tm * L::BM, tn * kTileCols, acc);
+    mainloop_small<NXB, NWB, kGated, !OUT_BF16>(p, lds, c, tm * L::BM, tn * kTileCols, acc);
     epilogue<NXB, NWB, OUT_BF16, HAS_BIAS, ACT, true>(p, reinterpret_cast<uint16_t *>(lds), c, tm * L::BM, tn * kTileCols, acc);
 }
 
