@@ -12,15 +12,16 @@ namespace {
 
 // Tiles for more than kFp8NarrowMaxM rows: the candidate with the least
 // (0.2 r + 0.8 ceil r) x (time of one round), r = rounds of tiles over the CUs, at least 1 (a partly
-// filled last round runs a little faster than a full one).  The times are those of K = 6144 with
-// the weights in HBM, in us; the choice was checked against sweeps of every shape, 97 to 8192 rows, K 640 to
-// 8192.  bf16 output (8-bit products): 4608 x 9216 x 6144 takes 224 x 256 (2.95 rounds, 184 us against
-// 190 in 256 x 256), 4608 x 4608 x 6144 224 x 192 (1.97 rounds, 116 against 144), 8192^3 256 x 256
-// (369 against 393 to 471).  fp32 output (exact products): 4608 x 6144 x 4608 takes 224 x 256 (174 us
-// against 183 in 256 x 256 and 182 in 192 x 192), 1024 x 4608 x 6144 192 x 192 (71 against 99 in 224 x
-// 256 and 94 in 128 x 128).  The eight-wave tiles of 128 and 64 rows by 128 columns keep more k-tiles in
-// flight and run the few hundred rows that leave most CUs idle otherwise: 333 x 6144 x 4608 (fp32) 38
-// us in 128 x 128 against 54 in 192 x 192, 129 x 4608 x 6144 32 us in 64 x 128 against 69.
+// filled last round runs a little faster than a full one).  The times are those of K = 6144 in us,
+// between a lone round with its weights in HBM and full rounds; the choice was checked against sweeps of
+// every shape, 97 to 8192 rows, K 640 to 8192.  bf16 output (8-bit products): 4608 x 9216 x 6144 takes
+// 224 x 256 (2.95 rounds, 184 us against 190 in 256 x 256 and 219 in 192 x 192), 4608 x 2304 x 6144 224 x 192
+// (one round, 57 us against 81 in 192 x 192), 8192^3 256 x 256 (369 against 393 in 224 x 256).  fp32 output (exact
+// products): 4608 x 6144 x 4608 takes 224 x 256 (174 us against 183 in 256 x 256 and 182 in 192 x
+// 192), 1024 x 4608 x 6144 192 x 192 (71 against 99 in 224 x 256 and 94 in 128 x 128).  The eight-wave
+// tiles of 128 and 64 rows by 128 columns run the few hundred rows that leave most CUs idle otherwise:
+// 333 x 6144 x 4608 24 us in 128 x 128 against 34 in 192 x 192 (bf16; fp32 38 against 54), 129 x 4608 x
+// 6144 21 us in 64 x 128 against 44 (fp32 32 against 69).
 struct TileChoice {
     int nxb, nwb;  // nwb == 2: the eight-wave kernel
 };
@@ -31,8 +32,8 @@ TileChoice pick_tile(const Fp8Problem &p)
         int nxb, nwb;
         double time;
     };
-    static const Cand kEight[] = {{8, 8, 75}, {7, 8, 71}, {7, 6, 60}, {6, 6, 55}, {4, 2, 33}, {2, 2, 24.5}};
-    static const Cand kEightGated[] = {{8, 8, 75}, {7, 8, 71}, {6, 8, 68}, {4, 2, 33}, {2, 2, 24.5}};
+    static const Cand kEight[] = {{8, 8, 68}, {7, 8, 64}, {7, 6, 53}, {6, 6, 45}, {4, 2, 33}, {2, 2, 24.5}};
+    static const Cand kEightGated[] = {{8, 8, 68}, {7, 8, 64}, {6, 8, 62}, {4, 2, 31.5}, {2, 2, 24.5}};
     static const Cand kExact[] = {{8, 8, 109}, {7, 8, 99}, {6, 6, 70.5}, {4, 2, 49.5}, {2, 2, 33.5}};
     static const Cand kExactGated[] = {{8, 8, 109}, {7, 8, 99}, {4, 2, 49.5}, {2, 2, 33.5}};
     const Cand *first = p.out_bf16 ? (p.swiglu ? kEightGated : kEight) : (p.swiglu ? kExactGated : kExact);

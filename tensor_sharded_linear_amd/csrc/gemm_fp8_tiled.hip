@@ -58,15 +58,15 @@ __device__ __forceinline__ void scaled_mfma(f32x4 &acc, const i32x8 &w, const i3
 #undef TPL_SCALED_MFMA
 }
 
-// What both main loops share: two LDS stages of X and W tiles (rows of 128 codes, 16-byte chunk c of
+// What both main loops share: S LDS stages of X and W tiles (rows of 128 codes, 16-byte chunk c of
 // row r at c ^ ((r >> 1) & 7)), the loads that fill them, and the scales.  k-tile u is in stage
-// u % 2; past the last k-tile the loads repeat it into a stage that is never read again.
-template <int NXB, int NWB, bool GATED>
+// u % S; past the last k-tile the loads repeat it into a stage that is never read again.
+template <int NXB, int NWB, bool GATED, int S>
 struct Feed {
     static constexpr int WM = 16 * NXB, WN = 16 * NWB, BM = 2 * WM, BN = 2 * WN;
     static constexpr int kXBytes = BM * kRow, kWBytes = BN * kRow;
     static constexpr int kDmaX = BM / 32, kDmaW = BN / 32, kDma = kDmaX + kDmaW;  // per lane and k-tile
-    static constexpr int kLdsBytes = 2 * (kXBytes + kWBytes) + 4096;
+    static constexpr int kLdsBytes = S * (kXBytes + kWBytes) + 4096;
     static_assert(!GATED || NWB == 8, "the gated tile pairs four gate and four up blocks per wave");
 
     char *base;
@@ -108,23 +108,23 @@ struct Feed {
         wsoff = (uint32_t)wrow(min(srow, BN - 1)) * (uint32_t)p.ldws;
         const int fr = c.lane & 15;
         xl = base + (c.wave_m * WM + fr) * kRow;
-        wl = base + 2 * kXBytes + (c.wave_n * WN + fr) * kRow;
-        xsl = base + 2 * (kXBytes + kWBytes) + (c.wave_m * WM + fr) * 4;
-        wsl = base + 2 * (kXBytes + kWBytes) + 1024 + (c.wave_n * WN + fr) * 4;
+        wl = base + S * kXBytes + (c.wave_n * WN + fr) * kRow;
+        xsl = base + S * (kXBytes + kWBytes) + (c.wave_m * WM + fr) * 4;
+        wsl = base + S * (kXBytes + kWBytes) + 1024 + (c.wave_n * WN + fr) * 4;
     }
-    __device__ __forceinline__ void dma_x(int d, int u) const
+    __device__ __forceinline__ void dma_x(int d, int u, int stage) const
     {
         dma16_sbase(xbase + min(u, T - 1) * kRow, xoff[d],
-                    reinterpret_cast<uint16_t *>(base + (u & 1) * kXBytes + (d * 4 + wave) * 1024));
+                    reinterpret_cast<uint16_t *>(base + stage * kXBytes + (d * 4 + wave) * 1024));
     }
-    __device__ __forceinline__ void dma_w(int d, int u) const
+    __device__ __forceinline__ void dma_w(int d, int u, int stage) const
     {
         dma16_sbase(wbase + min(u, T - 1) * kRow, woff[d],
-                    reinterpret_cast<uint16_t *>(base + 2 * kXBytes + (u & 1) * kWBytes + (d * 4 + wave) * 1024));
+                    reinterpret_cast<uint16_t *>(base + S * kXBytes + stage * kWBytes + (d * 4 + wave) * 1024));
     }
     __device__ __forceinline__ void dma_scales(int group) const
     {
-        char *d = base + 2 * (kXBytes + kWBytes) + (group & 1) * 2048 + wave * 256;
+        char *d = base + S * (kXBytes + kWBytes) + (group & 1) * 2048 + wave * 256;
         const int at = 4 * min(group, groups - 1);
         dma4_sbase(xsbase + at, xsoff, d);
         dma4_sbase(wsbase + at, wsoff, d + 1024);
@@ -136,12 +136,21 @@ struct Feed {
     }
 };
 
+__device__ __forceinline__ uint32_t lds_address(const char *p)
+{
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+}
+__device__ __forceinline__ i32x4 lds_read16(uint32_t at)
+{
+    return *(__attribute__((address_space(3))) const i32x4 *)at;
+}
+
 // acc += X[m0 .., :] . W[n0 .., :]^T on the 8-bit matrix cores.
-template <int NXB, int NWB, bool GATED>
+template <int NXB, int NWB, bool GATED, int S>
 __device__ __forceinline__ void mainloop8(const Fp8Params &p, char *lds, const Ctx &c, int m0, int n0,
                                           f32x4 (&acc)[NXB][NWB])
 {
-    typedef Feed<NXB, NWB, GATED> F;
+    typedef Feed<NXB, NWB, GATED, S> F;
     constexpr int kDmaW = F::kDmaW, kDma = F::kDma;
     constexpr int kMfma = NXB * NWB, kLast = kMfma - NXB;  // first MFMA of the last W block
     constexpr int RS = (NWB - 1) / 2;                      // X reads: one every RS MFMAs
@@ -151,20 +160,29 @@ __device__ __forceinline__ void mainloop8(const Fp8Params &p, char *lds, const C
     static_assert(NXB >= 5, "the scale reads are placed within a W block");
     const F f(p, lds, c, m0, n0);
     const int T = f.T;
-    // load d of the step after barrier u: W of k-tile u + 2, X of k-tile u + 3
-    auto dma = [&](int d, int u) {
+    // load d of the step after barrier u: W of k-tile u + S into the stage of k-tile u, X of k-tile
+    // u + S + 1 into that of k-tile u + 1 (whose X fragments every wave has read by then)
+    auto dma = [&](int d, int u, int stage, int next) {
         if (d < kDmaW)
-            f.dma_w(d, u + 2);
+            f.dma_w(d, u + S, stage);
         else
-            f.dma_x(d - kDmaW, u + 3);
+            f.dma_x(d - kDmaW, u + S + 1, next);
     };
     // Fragments: lane l holds 32 codes of row l % 16 of a block, chunks l / 16 and 4 + l / 16.  Which
     // features these are does not matter, as both operands take the same ones.
     const int g = c.lane >> 4, swz = (c.lane >> 1) & 7;
     const int c0 = (g ^ swz) * 16, c1 = ((4 + g) ^ swz) * 16;
-    auto read = [&](const char *t, int block, int half) {
-        return *reinterpret_cast<const i32x4 *>(t + block * 16 * kRow + (half ? c1 : c0));
+    // the lane's first chunks in a tile of a stage; opaque, or the compiler keeps an address a block
+    struct At {
+        uint32_t half[2];
     };
+    auto at = [&](const char *t, int stage, int bytes) {
+        At a{{lds_address(t) + stage * bytes + c0, lds_address(t) + stage * bytes + c1}};
+        if constexpr (S > 2)
+            asm volatile("" : "+v"(a.half[0]), "+v"(a.half[1]));
+        return a;
+    };
+    auto read = [&](const At &a, int block, int half) { return lds_read16(a.half[half] + block * 16 * kRow); };
     auto set = [](i32x8 &f, int half, i32x4 v) {
         if (half == 0)
             f = __builtin_shufflevector(__builtin_shufflevector(v, v, 0, 1, 2, 3, 0, 1, 2, 3), f, 0, 1, 2, 3, 12, 13, 14, 15);
@@ -173,56 +191,64 @@ __device__ __forceinline__ void mainloop8(const Fp8Params &p, char *lds, const C
     };
     uint32_t sx[NXB], sw[NWB];
 
-    // prologue
+    // prologue: what the first S - 1 k-tiles read
     i32x8 fa[NXB] = {}, fb[NXB] = {}, fw[2] = {};
-#pragma unroll
-    for (int d = 0; d < F::kDmaX; ++d)
-        f.dma_x(d, 0);
-#pragma unroll
-    for (int d = 0; d < kDmaW; ++d)
-        f.dma_w(d, 0);
-#pragma unroll
-    for (int d = 0; d < F::kDmaX; ++d)
-        f.dma_x(d, 1);
     f.dma_scales(0);
-    wait_dma_keep<0>();
+#pragma unroll
+    for (int d = 0; d < F::kDmaX; ++d)
+        f.dma_x(d, 0, 0);
+#pragma unroll
+    for (int u = 0; u < S - 1; ++u) {
+#pragma unroll
+        for (int d = 0; d < kDmaW; ++d)
+            f.dma_w(d, u, u);
+#pragma unroll
+        for (int d = 0; d < F::kDmaX; ++d)
+            f.dma_x(d, u + 1, u + 1);
+    }
+    wait_dma_keep<(S - 2) * kDma>();
     barrier_only();
 #pragma unroll
     for (int i = 0; i < NXB; ++i) {
-        set(fa[i], 0, read(f.xl, i, 0));
-        set(fa[i], 1, read(f.xl, i, 1));
+        set(fa[i], 0, read(at(f.xl, 0, 0), i, 0));
+        set(fa[i], 1, read(at(f.xl, 0, 0), i, 1));
         sx[i] = F::scale(f.xsl, 0, i);
     }
-    set(fw[0], 0, read(f.wl, 0, 0));
-    set(fw[0], 1, read(f.wl, 0, 1));
+    set(fw[0], 0, read(at(f.wl, 0, 0), 0, 0));
+    set(fw[0], 1, read(at(f.wl, 0, 0), 0, 1));
 #pragma unroll
     for (int j = 0; j < NWB; ++j)
         sw[j] = F::scale(f.wsl, 0, j);
-    wait_dma_keep<0>();
+    wait_dma_keep<(S - 2) * kDma>();
     barrier_only();
 #pragma unroll
     for (int d = 0; d < kF; ++d)
-        dma(d, -1);
+        dma(d, -1, S - 1, 0);
+    int before = S - 1, stage = 0, after = 1;  // stages of k-tiles t - 1, t, t + 1
     int t = 0;
-    // k-tile t, with S = t % 4
-    auto body = [&](i32x8 (&cur)[NXB], i32x8 (&nxt)[NXB], auto S) __attribute__((always_inline)) {
-        constexpr int st = decltype(S)::value, par = st & 1;
-        const char *xn = f.xl + (par ^ 1) * F::kXBytes;          // X of k-tile t + 1
-        const char *wc = f.wl + par * F::kWBytes, *wn = f.wl + (par ^ 1) * F::kWBytes;
+    // k-tile t, with T4 = t % 4
+    auto body = [&](i32x8 (&cur)[NXB], i32x8 (&nxt)[NXB], auto T4) __attribute__((always_inline)) {
+        constexpr int st = decltype(T4)::value;
+        // three stages: uniform values that the compiler has to be told are uniform
+        const int s0 = S == 2 ? st & 1 : __builtin_amdgcn_readfirstlane(stage);
+        const int s1 = S == 2 ? (st & 1) ^ 1 : __builtin_amdgcn_readfirstlane(after);
+        const int sb = S == 2 ? s1 : __builtin_amdgcn_readfirstlane(before);
+        const At xn = at(f.xl, s1, F::kXBytes);  // X of k-tile t + 1
+        const At wc = at(f.wl, s0, F::kWBytes), wn = at(f.wl, s1, F::kWBytes);
         const int buf = (t >> 2) & 1;  // of this k-tile's scales
         each([&](auto Q) __attribute__((always_inline)) {
             constexpr int q = decltype(Q)::value, j = q / NXB, i = q % NXB;
-            if constexpr (q == kLast) {
-                wait_dma_keep<0>();
+            if constexpr (q == kLast) {  // W of k-tile t + 1 and X of k-tile t + 2 have landed
+                wait_dma_keep<(S - 2) * kDma>();
                 barrier_only();
             }
             scaled_mfma<st>(acc[i][j], fw[j & 1], cur[i], sw[j], sx[i]);
             // loads: the rest of the step after the previous barrier, then the first of this one's
             if constexpr (q < kLast) {
                 if constexpr (q % DS == 0 && kF + q / DS < kDma)
-                    dma(kF + q / DS, t - 1);
+                    dma(kF + q / DS, t - 1, sb, s0);
             } else if constexpr ((q - kLast) % DS == 0 && (q - kLast) / DS < kF) {
-                dma((q - kLast) / DS, t);
+                dma((q - kLast) / DS, t, s0, s1);
             }
             // fragments: X of the next k-tile, the next W block
             if constexpr (q % RS == 0 && q / RS < 2 * NXB)
@@ -245,6 +271,9 @@ __device__ __forceinline__ void mainloop8(const Fp8Params &p, char *lds, const C
             if constexpr (st == 1 && q == NXB)
                 f.dma_scales(t / 4 + 1);
         }, std::make_integer_sequence<int, kMfma>{});
+        before = stage;
+        stage = after;
+        after = after == S - 1 ? 0 : after + 1;
     };
     for (;;) {
         body(fa, fb, std::integral_constant<int, 0>{});
@@ -306,7 +335,7 @@ template <int NXB, int NWB, bool GATED>
 __device__ __forceinline__ void mainloop_exact(const Fp8Params &p, char *lds, const Ctx &c, int m0, int n0,
                                                f32x4 (&acc)[NXB][NWB])
 {
-    typedef Feed<NXB, NWB, GATED> F;
+    typedef Feed<NXB, NWB, GATED, 2> F;
     constexpr int kDma = F::kDma, kDmaX = F::kDmaX, kMfma = NXB * NWB;
     constexpr int kCx = NXB + NWB - 4;                    // slot of the first X conversions, two a slot
     constexpr int kCw = kCx + 2 * NXB;                    // and of the W conversions
@@ -316,11 +345,11 @@ __device__ __forceinline__ void mainloop_exact(const Fp8Params &p, char *lds, co
                   "the last in-place W conversion ends within the step");
     const F f(p, lds, c, m0, n0);
     const int T = f.T;
-    auto dma = [&](int d, int u) {
+    auto dma = [&](int d, int u, int stage) {
         if (d < kDmaX)
-            f.dma_x(d, u);
+            f.dma_x(d, u, stage);
         else
-            f.dma_w(d - kDmaX, u);
+            f.dma_w(d - kDmaX, u, stage);
     };
     // Step s: lanes 16 g .. 16 g + 15 take half g % 2 of chunk 2 s + g / 2 of their rows, so 32 neighbouring
     // lanes read whole chunks and meet every LDS bank once.
@@ -343,7 +372,7 @@ __device__ __forceinline__ void mainloop_exact(const Fp8Params &p, char *lds, co
 
 #pragma unroll
     for (int d = 0; d < kDma; ++d)
-        dma(d, 0);
+        dma(d, 0, 0);
     f.dma_scales(0);
     wait_dma_keep<0>();
     barrier_only();
@@ -369,7 +398,7 @@ __device__ __forceinline__ void mainloop_exact(const Fp8Params &p, char *lds, co
     }, std::make_integer_sequence<int, 4>{});
 #pragma unroll
     for (int d = 0; d < kD0; ++d)
-        dma(d, 1);
+        dma(d, 1, 1);
     asm volatile("s_nop 1" ::: "memory");
     int t = 0;
     auto step = [&](i32x4 (&cur)[NXB], i32x4 (&nxt)[NXB], auto S, auto PAR) __attribute__((always_inline)) {
@@ -393,9 +422,9 @@ __device__ __forceinline__ void mainloop_exact(const Fp8Params &p, char *lds, co
                 rw[q - NXB] = read_w(q - NXB, sn, stage);
             // k-tile t + 2 into k-tile t's stage: half of the loads here, half in the next k-tile's step 0
             if constexpr (s == 3 && q % (kMfma / kD0) == 1 && q / (kMfma / kD0) < kD0)
-                dma(q / (kMfma / kD0), t + 2);
+                dma(q / (kMfma / kD0), t + 2, par);
             if constexpr (s == 0 && q % (kMfma / kD1) == 1 && q / (kMfma / kD1) < kD1)
-                dma(kD0 + q / (kMfma / kD1), t + 1);
+                dma(kD0 + q / (kMfma / kD1), t + 1, par ^ 1);
             // the next k-tile's scales: dwords in step 2, factors in step 3
             if constexpr (s == 2 && q >= kCw && q < kCw + NXB)
                 dx[q - kCw] = F::scale(f.xsl, ((t + 1) >> 2) & 1, q - kCw);
@@ -456,7 +485,9 @@ void gemm_fp8_nt_kernel(Fp8Params p)
 {
     constexpr bool kGated = ACT == kActSwiglu;
     constexpr int BM = 32 * NXB, BN = 32 * NWB, kTileCols = kGated ? BN / 2 : BN;
-    __shared__ __attribute__((aligned(1024))) char lds[Feed<NXB, NWB, kGated>::kLdsBytes];
+    // three stages where they fit in the 160 KiB of LDS (224 x 192 and 192 x 192)
+    constexpr int S = !EXACT && Feed<NXB, NWB, kGated, 3>::kLdsBytes <= 160 * 1024 ? 3 : 2;
+    __shared__ __attribute__((aligned(1024))) char lds[Feed<NXB, NWB, kGated, S>::kLdsBytes];
     Ctx c;
     c.lane = threadIdx.x & 63;
     c.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -469,7 +500,7 @@ void gemm_fp8_nt_kernel(Fp8Params p)
     if constexpr (EXACT)
         mainloop_exact<NXB, NWB, kGated>(p, lds, c, tm * BM, tn * kTileCols, acc);
     else
-        mainloop8<NXB, NWB, kGated>(p, lds, c, tm * BM, tn * kTileCols, acc);
+        mainloop8<NXB, NWB, kGated, S>(p, lds, c, tm * BM, tn * kTileCols, acc);
     finish<NXB, NWB>(acc);
     epilogue<NXB, NWB, !EXACT, HAS_BIAS, ACT, true>(p, reinterpret_cast<uint16_t *>(lds), c, tm * BM, tn * kTileCols, acc);
 }
