@@ -29,6 +29,7 @@ from ._binding import (  # noqa: F401
 from ._block import (  # noqa: F401
     tp_block_norm,
     tp_linear_colwise_fp8,
+    tp_linear_fp8_tile_shape,
     tp_linear_rowwise_fp8,
     tp_quantize_fp8,
 )
@@ -37,6 +38,7 @@ __all__ = [
     "tp_linear_colwise", "tp_linear_rowwise", "tp_linear_rowwise_split_input", "tp_linear_tile_shape",
     "tp_fused_qkv_split", "tp_partial_combine",
     "tp_plan_shard_slice", "tp_plan_shard_shape", "tp_load_shard", "tp_load_shard_shape", "tp_last_error",
-    "tp_quantize_fp8", "tp_linear_colwise_fp8", "tp_linear_rowwise_fp8", "tp_block_norm",
+    "tp_quantize_fp8", "tp_linear_colwise_fp8", "tp_linear_rowwise_fp8",
+    "tp_linear_fp8_tile_shape", "tp_block_norm",
     "load_library", "TPError", "TPValueError", "TPRuntimeError", "TPIOError",
 ]

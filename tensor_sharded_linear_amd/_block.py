@@ -27,6 +27,7 @@ _P, _I64, _I, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
 _NORMS = {"none": 0, "layer": 1, "rms": 2}
 _ROWS = {torch.bfloat16: 0, torch.float32: 1, CODES: 2}
 _DT = _b._DT
+_ACTS = {"none": _b.TP_ACT_NONE, "gelu_tanh": _b.TP_ACT_GELU_TANH, "swiglu": _b.TP_ACT_SWIGLU}
 
 
 class _BlockNormArgs(ctypes.Structure):
@@ -51,6 +52,7 @@ SIGNATURES = {
     "tp_quantize_fp8": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _I64, _I64, _P]),
     "tp_linear_colwise_fp8": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I64, _I64, _I64, _P]),
     "tp_linear_rowwise_fp8": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P]),
+    "tp_linear_fp8_tile_shape": (_I, [_I64, _I64, _I64, _I, _I, ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
     "tp_block_norm": (_I, [_P, _P]),
 }
 
@@ -176,16 +178,16 @@ def tp_linear_colwise_fp8(x: torch.Tensor, x_scale: torch.Tensor, w_shard: torch
                           bias: Optional[torch.Tensor] = None, *, act: str = "none",
                           out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
                           stream=None) -> torch.Tensor:
-    """Colwise shard of quantized rows: ``out = act(x @ w_shard.T + bias)``, fp32 accumulation.
+    """Colwise shard of quantized rows: ``out = act(x @ w_shard.T + bias)``, fp32 accumulation
+    (fp32 output: exact products; bf16 output of more than 96 rows: the 8-bit matrix cores).
 
     ``x``/``x_scale`` and ``w_shard``/``w_scale`` as :func:`tp_quantize_fp8` gives them; ``act``,
     ``bias`` and ``out`` as :func:`tp_linear_colwise` (``"swiglu"``: a packed [gate; up] shard)."""
     lib = _library()
     m, rows, k, operands = _operands(x, x_scale, w_shard, w_scale)
-    try:
-        a = {"none": _b.TP_ACT_NONE, "gelu_tanh": _b.TP_ACT_GELU_TANH, "swiglu": _b.TP_ACT_SWIGLU}[act]
-    except KeyError:
-        raise ValueError("act must be 'none', 'gelu_tanh' or 'swiglu'") from None
+    if act not in _ACTS:
+        raise ValueError("act must be 'none', 'gelu_tanh' or 'swiglu'")
+    a = _ACTS[act]
     if a == _b.TP_ACT_SWIGLU and rows % 2:
         raise ValueError(f"a SwiGLU shard has an even number of rows [gate; up], got {rows}")
     n = rows // 2 if a == _b.TP_ACT_SWIGLU else rows
@@ -218,6 +220,21 @@ def tp_linear_rowwise_fp8(x_shard: torch.Tensor, x_scale: torch.Tensor, w_shard:
         _same_device(x_shard, out=out)
     _call(lib.tp_linear_rowwise_fp8, x_shard, stream, *operands, out.data_ptr(), _ld(out), m, n, k)
     return out
+
+
+def tp_linear_fp8_tile_shape(m: int, n: int, k: int, act: str = "none",
+                             out_dtype: torch.dtype = torch.bfloat16) -> tuple:
+    """(rows, cols) of the output tile that the products of quantized rows use for an [m, k] x
+    [n, k]^T problem on the current device; up to 96 rows the rows that the split-K kernel's instance
+    holds and the output columns of each workgroup.  For ``act="swiglu"`` n counts the outputs.
+    Host-only query: no device work."""
+    if act not in _ACTS:
+        raise ValueError("act must be 'none', 'gelu_tanh' or 'swiglu'")
+    if out_dtype not in _DT:
+        raise ValueError("out_dtype must be bf16 or fp32")
+    rows, cols = _I64(), _I64()
+    _check(_library().tp_linear_fp8_tile_shape(m, n, k, _ACTS[act], _DT[out_dtype], ctypes.byref(rows), ctypes.byref(cols)))
+    return rows.value, cols.value
 
 
 def _feature_vec(t: Optional[torch.Tensor], name: str, d: int, index: int) -> int:

@@ -16,6 +16,7 @@ FLAGS = [
     # keep the compiler from forming packed-fp32 (v_pk_*_f32) instructions
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
+    "-parallel-jobs=8",  # the sources side by side
 ]
 
 

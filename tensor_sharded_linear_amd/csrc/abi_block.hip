@@ -163,6 +163,33 @@ tp_status tp_linear_rowwise_fp8(const void *x, int64_t ldx, const void *x_scale,
     return run_fp8(fn, p, 4, stream);
 }
 
+tp_status tp_linear_fp8_tile_shape(int64_t M, int64_t N, int64_t K, tp_act act, tp_dtype y_dtype,
+                                   int64_t *tile_rows, int64_t *tile_cols)
+{
+    const char *fn = "tp_linear_fp8_tile_shape";
+    tpl::last_error_buffer()[0] = 0;
+    if (!tile_rows || !tile_cols)
+        return fail(TP_ERR_INVALID_ARG, "%s: tile_rows and tile_cols must be non-null", fn);
+    if (act != TP_ACT_NONE && act != TP_ACT_GELU_TANH && act != TP_ACT_SWIGLU)
+        return fail(TP_ERR_INVALID_ARG, "%s: act must be TP_ACT_NONE, TP_ACT_GELU_TANH or TP_ACT_SWIGLU", fn);
+    if (!is_dtype(y_dtype))
+        return fail(TP_ERR_INVALID_ARG, "%s: y_dtype must be TP_BF16 or TP_F32", fn);
+    if (M < 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+        return fail(TP_ERR_INVALID_ARG, "%s: need 0 <= M, 0 < N, 0 < K, all at most 2^30", fn);
+    tpl::Fp8Problem p{};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.out_bf16 = y_dtype == TP_BF16;
+    p.gelu = act == TP_ACT_GELU_TANH;
+    p.swiglu = act == TP_ACT_SWIGLU;
+    int rows = 0, cols = 0;
+    tpl::gemm_fp8_tile_shape(p, &rows, &cols);
+    *tile_rows = rows;
+    *tile_cols = cols;
+    return TP_OK;
+}
+
 tp_status tp_block_norm(const tp_block_norm_args *args, hipStream_t stream)
 {
     const char *fn = "tp_block_norm";

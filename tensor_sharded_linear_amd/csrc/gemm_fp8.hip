@@ -58,6 +58,18 @@ TileChoice pick_tile(const Fp8Problem &p)
 
 }  // namespace
 
+void gemm_fp8_tile_shape(const Fp8Problem &p, int *rows, int *cols)
+{
+    if (p.M <= kFp8NarrowMaxM) {
+        *rows = (int)((p.M + 15) / 16) * 16;
+        *cols = gemm_fp8_narrow_cols(p);
+        return;
+    }
+    const TileChoice c = pick_tile(p);
+    *rows = 32 * c.nxb;
+    *cols = (c.nwb == 2 ? 128 : 32 * c.nwb) / (p.swiglu ? 2 : 1);
+}
+
 hipError_t launch_gemm_fp8(const Fp8Problem &p, hipStream_t stream)
 {
     if (p.M > kFp8NarrowMaxM) {

@@ -271,6 +271,8 @@ int pick_rows(const Fp8Problem &p, int cus)
 
 }  // namespace
 
+int gemm_fp8_narrow_cols(const Fp8Problem &p) { return pick_rows(p, cu_count()); }
+
 hipError_t launch_gemm_fp8_narrow(const Fp8Problem &pr, hipStream_t stream)
 {
     NarrowParams np;

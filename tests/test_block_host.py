@@ -96,6 +96,19 @@ def test_colwise_refusals():
     assert "2 GiB" in tsl.tp_last_error()
 
 
+def test_tile_shape_query():
+    assert tsl.tp_linear_fp8_tile_shape(1, 9216, 6144) == (16, 36)
+    assert tsl.tp_linear_fp8_tile_shape(96, 9216, 6144, "none", torch.float32) == (96, 36)
+    rows, cols = tsl.tp_linear_fp8_tile_shape(4608, 9216, 6144, "gelu_tanh")
+    assert rows in (192, 224, 256) and cols in (192, 256)
+    for bad in (dict(m=-1), dict(n=0), dict(k=0), dict(k=1 << 31), dict(act="relu"), dict(out_dtype=torch.float16)):
+        with pytest.raises(ValueError):
+            tsl.tp_linear_fp8_tile_shape(**{**dict(m=4, n=64, k=128), **bad})
+    one = ctypes.c_int64()
+    assert K._library().tp_linear_fp8_tile_shape(4, 64, 128, 0, 0, None, ctypes.byref(one)) == INV
+    assert tsl.tp_last_error().startswith("tp_linear_fp8_tile_shape")
+
+
 def test_empty_is_a_no_op():
     assert quantize(M=0, x=None, codes=None, scales=None) == B.TP_OK
     assert linear(M=0, x=None, xs=None, y=None) == B.TP_OK

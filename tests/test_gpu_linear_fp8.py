@@ -56,7 +56,7 @@ def test_epilogues_within_the_derived_bound(m, act, bias, out):
     b = torch.randn(rows, generator=g).to(BF).cuda() if bias else None
     y = tsl.tp_linear_colwise_fp8(*x, *w, b, act=act, out_dtype=out)
     assert y.dtype == out
-    ref.check(y, *ref.linear(ref.values(*x), ref.values(*w), b, act), what=f"{m} {act}")
+    ref.check(y, *ref.linear(ref.values(*x), ref.values(*w), b, act, out == BF and m > 96), what=f"{m} {act}")
 
 
 @pytest.mark.parametrize("m,n,k", [(700, 1040, 2304), (1500, 2320, 768), (4608, 272, 128), (90, 4624, 512),
@@ -134,6 +134,38 @@ def test_scales_over_their_whole_range(m):
     w = _pair(wc, (127 - e + torch.randint(-2, 3, (n, 4), generator=g)).to(torch.uint8))
     y = tsl.tp_linear_rowwise_fp8(*x, *w)
     ref.check(y, *ref.linear(ref.values(*x), ref.values(*w), None, "none"))
+
+
+# One ragged problem for every tile that exists: (m, n, act, output, tile rows, tile columns).  The last
+# row and column tiles are partial, and K is three scale blocks: the scale dword's last byte is padding.
+TILES = [(2290, 6128, "none", BF, 256, 256), (4600, 9200, "gelu_tanh", BF, 224, 256), (4600, 2288, "none", BF, 224, 192),
+         (1000, 4592, "gelu_tanh", BF, 192, 192), (333, 6128, "none", BF, 128, 128), (129, 4592, "none", BF, 64, 128),
+         (4600, 4592, "swiglu", BF, 224, 128), (4090, 2032, "swiglu", BF, 256, 128), (4600, 2288, "swiglu", BF, 192, 128),
+         (333, 4592, "swiglu", BF, 128, 64), (129, 2288, "swiglu", BF, 64, 64), (2290, 6128, "none", F32, 256, 256),
+         (4600, 9200, "gelu_tanh", F32, 224, 256), (1000, 4592, "none", F32, 192, 192), (333, 6128, "gelu_tanh", F32, 128, 128),
+         (129, 4592, "none", F32, 64, 128), (4600, 4592, "swiglu", F32, 224, 128), (4090, 2032, "swiglu", F32, 256, 128),
+         (333, 4592, "swiglu", F32, 128, 64), (129, 2288, "swiglu", F32, 64, 64)]
+
+
+@pytest.mark.parametrize("m,n,act,out,rows,cols", TILES)
+@pytest.mark.parametrize("k", [384, 1152])
+def test_every_tile_with_ragged_edges(m, n, act, out, rows, cols, k):
+    """Integer operands, so that sums are exact; the activation's bound is that of ref.linear."""
+    assert tsl.tp_linear_fp8_tile_shape(m, n, k, act, out) == (rows, cols)
+    g = torch.Generator().manual_seed(m + n)
+    x, w = _integers(g, m, k), _integers(g, 2 * n if act == "swiglu" else n, k)
+    b = torch.randint(-8, 9, (w[0].shape[0],), generator=g).to(BF).cuda()
+    y = tsl.tp_linear_colwise_fp8(*x, *w, b, act=act, out_dtype=out).double()
+    s = ref.values(*x).cuda() @ ref.values(*w).cuda().t().contiguous() + b.double()
+    if act == "none":
+        assert torch.equal(y, s.to(out).double())
+        return
+    if act == "gelu_tanh":
+        want = 0.5 * s * (1 + torch.tanh((2 / torch.pi) ** 0.5 * (s + 0.044715 * s ** 3)))
+    else:
+        want = s[:, :n] * torch.sigmoid(s[:, :n]) * s[:, n:]
+    bound = 1e-5 * (1 + want.abs()) * 1.01 + ref.HALF_STEP[out] * want.abs()
+    assert bool(((y - want).abs() <= bound).all())
 
 
 def test_no_rows_is_a_no_op():
