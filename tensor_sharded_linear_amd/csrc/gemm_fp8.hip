@@ -61,8 +61,7 @@ TileChoice pick_tile(const Fp8Problem &p)
 void gemm_fp8_tile_shape(const Fp8Problem &p, int *rows, int *cols)
 {
     if (p.M <= kFp8NarrowMaxM) {
-        *rows = (int)((p.M + 15) / 16) * 16;
-        *cols = gemm_fp8_narrow_cols(p);
+        gemm_fp8_narrow_shape(p, rows, cols);
         return;
     }
     const TileChoice c = pick_tile(p);

@@ -37,7 +37,8 @@ struct NarrowParams {
     void *y;
     int64_t ldx, ldw, ldxs, ldws, ldy;
     int M, N, K;
-    int rows;  // output columns per workgroup, a multiple of 4
+    int rows;    // output columns per workgroup, a multiple of 4
+    int m_rows;  // activation rows per workgroup
     bool gelu;
 };
 
@@ -91,13 +92,14 @@ void gemm_fp8_narrow_kernel(NarrowParams p)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * p.rows, n_end = min(n0 + p.rows, p.N);
+    const int m0 = blockIdx.y * p.m_rows, m_end = min(m0 + p.m_rows, p.M);
     const int steps = (p.K / kQBlock - wave + kWavesN4 - 1) / kWavesN4;
     char *ring = lds + wave * (D * R::kStep);
     // Row r of block b, W blocks first; rows past the end repeat the last one.
     const auto wrow = [&](int b, int r) {
         return GATED ? b / kHalf * p.N + min(n0 + 16 * (b % kHalf) + r, n_end - 1) : min(n0 + 16 * b + r, n_end - 1);
     };
-    const auto xrow = [&](int b, int r) { return min(16 * (b - NB) + r, p.M - 1); };
+    const auto xrow = [&](int b, int r) { return min(m0 + 16 * (b - NB) + r, m_end - 1); };
     uint32_t off[kBlocks][2];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
@@ -194,8 +196,8 @@ void gemm_fp8_narrow_kernel(NarrowParams p)
     };
     for (int e = threadIdx.x; e < kItems; e += kThreadsN) {
         const int l = e & 63, mb = (e >> 6) / kHalf, jb = (e >> 6) % kHalf, blk = mb * NB + jb;
-        const int m = 16 * mb + (l & 15), n = n0 + 16 * jb + 4 * (l >> 4);
-        if (m >= p.M || n >= n_end)
+        const int m = m0 + 16 * mb + (l & 15), n = n0 + 16 * jb + 4 * (l >> 4);
+        if (m >= m_end || n >= n_end)
             continue;
         f32x4 v = total(blk, l);
         if (p.bias)
@@ -224,7 +226,7 @@ void gemm_fp8_narrow_kernel(NarrowParams p)
 template <int MB, int NB, bool GATED>
 hipError_t launch_mb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
 {
-    const dim3 grid((np.N + np.rows - 1) / np.rows), block(kThreadsN);
+    const dim3 grid((np.N + np.rows - 1) / np.rows, (np.M + np.m_rows - 1) / np.m_rows), block(kThreadsN);
     if (out_bf16)
         hipLaunchKernelGGL((gemm_fp8_narrow_kernel<MB, NB, GATED, true>), grid, block, 0, stream, np);
     else
@@ -235,7 +237,7 @@ hipError_t launch_mb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
 template <int NB, bool GATED>
 hipError_t launch_nb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
 {
-    switch ((np.M + 15) / 16) {
+    switch ((np.m_rows + 15) / 16) {
     case 1: return launch_mb<1, NB, GATED>(np, out_bf16, stream);
     case 2: return launch_mb<2, NB, GATED>(np, out_bf16, stream);
     case 3: return launch_mb<3, NB, GATED>(np, out_bf16, stream);
@@ -244,26 +246,37 @@ hipError_t launch_nb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
     default:
         if constexpr (NB <= 3)
             return launch_mb<6, NB, GATED>(np, out_bf16, stream);
-        return hipErrorInvalidValue;  // pick_rows gives SwiGLU more than 80 rows at two blocks
+        return hipErrorInvalidValue;  // pick_runs gives SwiGLU more than 80 rows at two blocks
     }
 }
 
-// Output columns per workgroup: the CUs share the weight stream, and every workgroup also reads all
-// of X (from L2; a line costs about 0.6 of a weight line from HBM).  The LDS ring leaves room for
-// one workgroup per CU, so the cost of a choice is ceil(workgroups / CUs) x (weight rows + 0.6 M).
-// Ties go to more columns per workgroup.
-int pick_rows(const Fp8Problem &p, int cus)
+// Output columns and activation rows per workgroup.  Every workgroup streams its weight rows (from
+// HBM) and its activation rows (from L2, like weight rows that another workgroup reads too) through one
+// CU, and the LDS ring leaves room for one workgroup per CU: the cost of a choice is ceil(workgroups / CUs)
+// x (weight rows + 0.8 x activation rows).  One chunk of rows up to a few dozen; 77 x 4608 x 6144 takes
+// two chunks of 39 rows by 36 columns (256 workgroups: 15.9 us against 17.8 for 231 of all rows by 20).
+// Ties go to fewer chunks, then to more columns.
+struct Runs {
+    int cols, m_rows;
+};
+
+Runs pick_runs(const Fp8Problem &p, int cus)
 {
-    // MB + NB <= 9 blocks fit the ring: three, or with SwiGLU, which pairs them, four up to 80 rows
-    const int max_rows = p.swiglu ? (p.M <= 80 ? 32 : 16) : 48;
-    int best = 4;
+    Runs best{4, (int)p.M};
     double best_cost = -1;
-    for (int rows = 4; rows <= max_rows; rows += 4) {
-        const int64_t wgs = (p.N + rows - 1) / rows;
-        const double cost = (double)((wgs + cus - 1) / cus) * ((p.swiglu ? 2 : 1) * rows + 0.6 * (double)p.M);
-        if (best_cost < 0 || cost <= best_cost) {
-            best = rows;
-            best_cost = cost;
+    for (int chunks = 1; chunks <= 4; ++chunks) {
+        const int m_rows = (int)((p.M + chunks - 1) / chunks);
+        if (chunks > 1 && m_rows < 16)
+            break;
+        // MB + NB <= 9 blocks fit the ring: three, or with SwiGLU, which pairs them, four up to 80 rows
+        const int max_cols = p.swiglu ? (m_rows <= 80 ? 32 : 16) : 48;
+        for (int cols = max_cols; cols >= 4; cols -= 4) {
+            const int64_t wgs = (p.N + cols - 1) / cols * ((p.M + m_rows - 1) / m_rows);
+            const double cost = (double)((wgs + cus - 1) / cus) * ((p.swiglu ? 2 : 1) * cols + 0.8 * m_rows);
+            if (best_cost < 0 || cost < best_cost) {
+                best = Runs{cols, m_rows};
+                best_cost = cost;
+            }
         }
     }
     return best;
@@ -271,7 +284,12 @@ int pick_rows(const Fp8Problem &p, int cus)
 
 }  // namespace
 
-int gemm_fp8_narrow_cols(const Fp8Problem &p) { return pick_rows(p, cu_count()); }
+void gemm_fp8_narrow_shape(const Fp8Problem &p, int *rows, int *cols)
+{
+    const Runs r = pick_runs(p, cu_count());
+    *rows = (r.m_rows + 15) / 16 * 16;
+    *cols = r.cols;
+}
 
 hipError_t launch_gemm_fp8_narrow(const Fp8Problem &pr, hipStream_t stream)
 {
@@ -290,7 +308,9 @@ hipError_t launch_gemm_fp8_narrow(const Fp8Problem &pr, hipStream_t stream)
     np.M = (int)pr.M;
     np.N = (int)pr.N;
     np.K = (int)pr.K;
-    np.rows = pick_rows(pr, cu_count());
+    const Runs runs = pick_runs(pr, cu_count());
+    np.rows = runs.cols;
+    np.m_rows = runs.m_rows;
     np.gelu = pr.gelu;
     if (pr.swiglu)
         return np.rows <= 16 ? launch_nb<2, true>(np, pr.out_bf16, stream) : launch_nb<4, true>(np, pr.out_bf16, stream);
