@@ -240,7 +240,8 @@ def tp_linear_fp8_tile_shape(m: int, n: int, k: int, act: str = "none",
 def _feature_vec(t: Optional[torch.Tensor], name: str, d: int, index: int) -> int:
     if t is None:
         return 0
-    if t.get_device() != index or t.dtype != torch.bfloat16 or t.shape != (d,) or (d > 1 and t.stride(0) != 1):
+    if t.get_device() != index or t.dtype != torch.bfloat16 or t.dim() != 1 or t.numel() != d or \
+            (d > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous bf16 vector of length {d} on cuda:{index}")
     return t.data_ptr()
 
@@ -325,23 +326,23 @@ def tp_block_norm(x: torch.Tensor, parts: Optional[Sequence[torch.Tensor]] = Non
             if z.shape != x.shape or z.get_device() != index:
                 raise ValueError(f"z_out must be [{m}, {d}] on {x.device}")
         z_args, z_rows = (z.data_ptr(), _ld(z), 0, 0), _ROWS[z_dtype]
-    tables, first = [], None
+    tables, first, groups = [], None, 0
     for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is None:
             tables.append((0, 0))
             continue
-        if t.dim() == 1:
-            t = t.unsqueeze(0)
-        if t.dim() != 2 or t.shape[1] != d or t.dtype not in _DT or t.get_device() != index or \
-                (d > 1 and t.stride(1) != 1):
+        rows, cols = t.shape if t.dim() == 2 else (1, t.numel())
+        if t.dim() not in (1, 2) or cols != d or t.dtype not in _DT or t.get_device() != index or \
+                (d > 1 and t.stride(-1) != 1):
             raise ValueError(f"{name} must be [groups, {d}] bf16 or fp32 on {x.device}, with unit column stride")
-        first = t if first is None else first
-        if t.dtype != first.dtype or t.shape[0] != first.shape[0]:
+        if first is None:
+            first, groups = t.dtype, rows
+        elif t.dtype != first or rows != groups:
             raise ValueError("gate, scale and shift must have one dtype and one number of groups")
-        tables.append((t.data_ptr(), _ld(t)))
-    groups, mod_dt, index_ptr = 0, 0, 0
+        tables.append((t.data_ptr(), t.stride(0) if rows > 1 else d))
+    mod_dt, index_ptr = 0, 0
     if first is not None:
-        mod_dt, groups = _DT[first.dtype], first.shape[0]
+        mod_dt = _DT[first]
         if group_index is not None:
             if group_rows is not None:
                 raise ValueError("pass group_rows or group_index, not both")

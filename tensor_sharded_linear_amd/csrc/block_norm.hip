@@ -215,11 +215,12 @@ __device__ __forceinline__ void normalise(float (&v)[U][8], const NormParams &p,
 }
 
 // One row per workgroup.  NP: the number of parts, or -1 for any.  TAIL: D is no multiple of 8.
-// THREADS: the most that it is launched with.  PRE: everything that a row reads is loaded ahead of its
-// use (not where 16 waves of a long row have 128 registers each).
-template <int U, int NP, bool TAIL, int THREADS, bool PRE>
-__global__ __launch_bounds__(THREADS) void block_norm_kernel(NormParams p)
+// With one unit a lane everything that a row reads is loaded ahead of its use; more units leave no room
+// for that in the 128 registers of a lane of 16 waves.
+template <int U, int NP, bool TAIL>
+__global__ __launch_bounds__(64 * kMaxWaves) void block_norm_kernel(NormParams p)
 {
+    constexpr bool PRE = U == 1;
     __shared__ float slots[4 * kMaxWaves];
     const int64_t row = p.row0 + blockIdx.x;
     const int parts = NP >= 0 ? NP : p.num_parts;
@@ -360,28 +361,26 @@ constexpr int64_t kRowsPerLaunch = (int64_t)1 << 21;
 
 typedef void (*NormKernel)(NormParams);
 
-// Up to 4 waves a row, or one unit a lane: everything ahead; the common part counts unrolled.
-template <int U, int THREADS>
+// One unit a lane: everything ahead; the common part counts unrolled.
 NormKernel eager_kernel(int parts, bool tail)
 {
     if (tail)
-        return parts == 0 ? block_norm_kernel<U, 0, true, THREADS, true> : block_norm_kernel<U, -1, true, THREADS, true>;
+        return parts == 0 ? block_norm_kernel<1, 0, true> : block_norm_kernel<1, -1, true>;
     switch (parts) {
-    case 0: return block_norm_kernel<U, 0, false, THREADS, true>;
-    case 1: return block_norm_kernel<U, 1, false, THREADS, true>;
-    case 2: return block_norm_kernel<U, 2, false, THREADS, true>;
-    case 4: return block_norm_kernel<U, 4, false, THREADS, true>;
-    default: return block_norm_kernel<U, -1, false, THREADS, true>;
+    case 0: return block_norm_kernel<1, 0, false>;
+    case 1: return block_norm_kernel<1, 1, false>;
+    case 2: return block_norm_kernel<1, 2, false>;
+    case 4: return block_norm_kernel<1, 4, false>;
+    default: return block_norm_kernel<1, -1, false>;
     }
 }
 
-// Longer rows: more than 4 waves of two to four units a lane.
 template <int U>
 NormKernel lean_kernel(int parts, bool tail)
 {
     if (tail)
-        return parts == 0 ? block_norm_kernel<U, 0, true, 1024, false> : block_norm_kernel<U, -1, true, 1024, false>;
-    return parts == 0 ? block_norm_kernel<U, 0, false, 1024, false> : block_norm_kernel<U, -1, false, 1024, false>;
+        return parts == 0 ? block_norm_kernel<U, 0, true> : block_norm_kernel<U, -1, true>;
+    return parts == 0 ? block_norm_kernel<U, 0, false> : block_norm_kernel<U, -1, false>;
 }
 
 }  // namespace
@@ -426,29 +425,22 @@ hipError_t launch_block_norm(const tp_block_norm_args &a, hipStream_t stream)
     p.mod_f32 = a.mod_dtype == TP_F32;
     p.residual = a.residual_scale;
     p.eps = a.eps;
-    // Units of 8 features per row and lane, and waves per row.  Few rows: as many waves as there are
-    // units, for the latency of one row; many rows: three or four units a lane, whichever leaves
-    // fewer lanes idle.
+    // Units of 8 features per lane, and waves per row.  One unit and as many waves as that takes is the
+    // fastest almost everywhere: the loads of many short waves overlap best (4608 x 6144, four parts,
+    // quantized z: 112 us against 119, 123 and 132 with two to four units; 7 rows of 6144: 4.0 us
+    // against 4.5 to 5.1).  Many long rows of at most one part do better with two (1024 x 6144: 18.5
+    // us against 21.2), and beyond 16 waves there is no choice.
     const int units = (p.D8 + 7) / 8;
     const auto waves_of = [&](int u) { return (units + 64 * u - 1) / (64 * u); };
-    int u = a.M <= cu_count() ? 1 : (waves_of(3) * 3 <= waves_of(4) * 4 ? 3 : 4);
+    int u = a.num_parts <= 1 && waves_of(1) > 8 && a.M > 2 * cu_count() ? 2 : 1;
     while (waves_of(u) > kMaxWaves)
         ++u;
     const int waves = waves_of(u);
-    while (u > 1 && waves_of(u - 1) == waves)
-        --u;
     const bool tail = p.D % 8 != 0;
-    NormKernel kernel;
-    if (waves <= 4)
-        kernel = u == 1   ? eager_kernel<1, 256>(p.num_parts, tail)
-                 : u == 2 ? eager_kernel<2, 256>(p.num_parts, tail)
-                 : u == 3 ? eager_kernel<3, 256>(p.num_parts, tail)
-                          : eager_kernel<4, 256>(p.num_parts, tail);
-    else
-        kernel = u == 1   ? eager_kernel<1, 1024>(p.num_parts, tail)
-                 : u == 2 ? lean_kernel<2>(p.num_parts, tail)
-                 : u == 3 ? lean_kernel<3>(p.num_parts, tail)
-                          : lean_kernel<4>(p.num_parts, tail);
+    const NormKernel kernel = u == 1   ? eager_kernel(p.num_parts, tail)
+                              : u == 2 ? lean_kernel<2>(p.num_parts, tail)
+                              : u == 3 ? lean_kernel<3>(p.num_parts, tail)
+                                       : lean_kernel<4>(p.num_parts, tail);
     for (p.row0 = 0; p.row0 < a.M; p.row0 += kRowsPerLaunch) {
         const dim3 grid((unsigned)(a.M - p.row0 < kRowsPerLaunch ? a.M - p.row0 : kRowsPerLaunch));
         hipLaunchKernelGGL(kernel, grid, dim3(64 * waves), 0, stream, p);
