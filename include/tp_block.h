@@ -93,8 +93,8 @@ tp_status tp_linear_rowwise_fp8(const void *x, int64_t ldx, const void *x_scale,
 /*
  * tp_linear_fp8_tile_shape -- host-only query of how the two products above run a problem of this
  * shape (K input features; for TP_ACT_SWIGLU, N counts the outputs) on the current device:
- * *tile_rows and *tile_cols receive the output tile of the tiled kernels (rows 256, 224, 192, 128 or
- * 64; columns 256, 192 or 128, half of that with SwiGLU), or, up to 96 rows, where the split-K
+ * *tile_rows and *tile_cols receive the output tile of the tiled kernels (rows 256, 224, 192, 128, 96
+ * or 64; columns 256, 192 or 128, half of that with SwiGLU), or, up to 96 rows, where the split-K
  * kernel runs, the rows that its instance holds (a multiple of 16) and the run of output columns (4 to
  * 48, at most 32 with SwiGLU) that each workgroup owns.
  * Errors: TP_ERR_INVALID_ARG for a null output pointer, an unknown act or y_dtype, or sizes

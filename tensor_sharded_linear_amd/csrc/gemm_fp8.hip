@@ -19,9 +19,9 @@ namespace {
 // (one round, 57 us against 81 in 192 x 192), 8192^3 256 x 256 (369 against 393 in 224 x 256).  fp32 output (exact
 // products): 4608 x 6144 x 4608 takes 224 x 256 (174 us against 183 in 256 x 256 and 182 in 192 x
 // 192), 1024 x 4608 x 6144 192 x 192 (71 against 99 in 224 x 256 and 94 in 128 x 128).  The eight-wave
-// tiles of 128 and 64 rows by 128 columns run the few hundred rows that leave most CUs idle otherwise:
-// 333 x 6144 x 4608 24 us in 128 x 128 against 34 in 192 x 192 (bf16; fp32 38 against 54), 129 x 4608 x
-// 6144 21 us in 64 x 128 against 44 (fp32 32 against 69).
+// tiles of 128, 96 and 64 rows by 128 columns run the few hundred rows that leave most CUs idle
+// otherwise: 333 x 6144 x 4608 21 us in 96 x 128 against 24 in 128 x 128 and 34 in 192 x 192 (bf16; fp32 33,
+// 38 and 54), 129 x 4608 x 6144 21 us in 64 x 128 against 44 in 192 x 192 (fp32 32 against 69).
 struct TileChoice {
     int nxb, nwb;  // nwb == 2: the eight-wave kernel
 };
@@ -32,12 +32,12 @@ TileChoice pick_tile(const Fp8Problem &p)
         int nxb, nwb;
         double time;
     };
-    static const Cand kEight[] = {{8, 8, 68}, {7, 8, 64}, {7, 6, 53}, {6, 6, 45}, {4, 2, 33}, {2, 2, 24.5}};
-    static const Cand kEightGated[] = {{8, 8, 68}, {7, 8, 64}, {6, 8, 62}, {4, 2, 31.5}, {2, 2, 24.5}};
-    static const Cand kExact[] = {{8, 8, 109}, {7, 8, 99}, {6, 6, 70.5}, {4, 2, 49.5}, {2, 2, 33.5}};
-    static const Cand kExactGated[] = {{8, 8, 109}, {7, 8, 99}, {4, 2, 49.5}, {2, 2, 33.5}};
+    static const Cand kEight[] = {{8, 8, 68}, {7, 8, 64}, {7, 6, 53}, {6, 6, 45}, {4, 2, 33}, {3, 2, 28.5}, {2, 2, 24.5}};
+    static const Cand kEightGated[] = {{8, 8, 68}, {7, 8, 64}, {6, 8, 62}, {4, 2, 31.5}, {3, 2, 28}, {2, 2, 24.5}};
+    static const Cand kExact[] = {{8, 8, 109}, {7, 8, 99}, {6, 6, 70.5}, {4, 2, 49.5}, {3, 2, 41}, {2, 2, 33.5}};
+    static const Cand kExactGated[] = {{8, 8, 109}, {7, 8, 99}, {4, 2, 49.5}, {3, 2, 41}, {2, 2, 33.5}};
     const Cand *first = p.out_bf16 ? (p.swiglu ? kEightGated : kEight) : (p.swiglu ? kExactGated : kExact);
-    const int count = p.out_bf16 ? (p.swiglu ? 5 : 6) : (p.swiglu ? 4 : 5);
+    const int count = p.out_bf16 ? (p.swiglu ? 6 : 7) : (p.swiglu ? 5 : 6);
     const int cus = cu_count();
     TileChoice best{8, 8};
     double best_cost = -1;

@@ -25,7 +25,8 @@ struct SmallParams {
 template <int NXB, int NWB>
 struct STile {
     static constexpr int WM = 16 * NXB, WN = 16 * NWB, BM = 2 * WM, BN = 4 * WN;
-    static constexpr int kStageBytes = (BM + BN) * kRow;
+    static constexpr int kPer = (BM + BN + 63) / 64;  // loads per wave and k-tile: 64 rows each, X then W
+    static constexpr int kStageBytes = kPer * 64 * kRow;
     static constexpr int kFit = (160 * 1024 - 4096) / kStageBytes;
     static constexpr int kStages = kFit > 5 ? 5 : kFit;
     static constexpr int kLdsBytes = kStages * kStageBytes + 4096;
@@ -62,7 +63,7 @@ __device__ __forceinline__ void mainloop_small(const SmallParams &p, char *lds, 
 {
     typedef STile<NXB, NWB> L;
     constexpr int BM = L::BM, BN = L::BN, S = L::kStages;
-    constexpr int kDmaX = BM / 64, kDmaW = BN / 64, kPer = kDmaX + kDmaW;
+    constexpr int kPer = L::kPer;
     static_assert(S >= 2 && (S - 1) * kPer <= 60, "the wait count fits vmcnt");
     // weight row of a tile row; gated: a wave column's first half holds gate rows, its second up rows
     auto wrow = [&](int r) {
@@ -75,9 +76,11 @@ __device__ __forceinline__ void mainloop_small(const SmallParams &p, char *lds, 
     const int dma_chunk = (c.lane & 7) ^ ((((c.wave & 1) << 2) + (c.lane >> 4)) & 7);
     uint32_t off[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-        off[j] = j < kDmaX ? (uint32_t)min(m0 + 64 * j + dma_row, p.M - 1) * (uint32_t)p.ldx + dma_chunk * 16
-                           : (uint32_t)wrow(64 * (j - kDmaX) + dma_row) * (uint32_t)p.ldw + dma_chunk * 16;
+    for (int j = 0; j < kPer; ++j) {
+        const int r = 64 * j + dma_row;  // rows past the W tile (a last load of half the waves) repeat its last
+        off[j] = r < BM ? (uint32_t)min(m0 + r, p.M - 1) * (uint32_t)p.ldx + dma_chunk * 16
+                        : (uint32_t)wrow(min(r - BM, BN - 1)) * (uint32_t)p.ldw + dma_chunk * 16;
+    }
     const int T = p.K / kRow, groups = (T + 3) / 4;
     const char *xbase = reinterpret_cast<const char *>(p.x), *wbase = reinterpret_cast<const char *>(p.w);
     auto issue = [&](int u, int stage) {
@@ -85,7 +88,7 @@ __device__ __forceinline__ void mainloop_small(const SmallParams &p, char *lds, 
         char *d = lds + stage * L::kStageBytes + c.wave * 1024;
 #pragma unroll
         for (int j = 0; j < kPer; ++j)
-            dma_to_lds16((j < kDmaX ? xbase : wbase) + k + off[j], d + j * 8192);
+            dma_to_lds16((64 * j + 8 * c.wave < BM ? xbase : wbase) + k + off[j], d + j * 8192);
     };
     // Scales of four k-tiles, a dword a row: the X tile's rows, then the W tile's; two buffers.
     char *sl = lds + S * L::kStageBytes;
@@ -234,8 +237,11 @@ hipError_t launch_tile(SmallParams gp, hipStream_t stream)
 template <bool OUT_BF16, bool HAS_BIAS, int ACT>
 hipError_t launch_shape(const SmallParams &gp, int nxb, hipStream_t stream)
 {
-    return nxb == 2 ? launch_tile<2, 2, OUT_BF16, HAS_BIAS, ACT>(gp, stream)
-                    : launch_tile<4, 2, OUT_BF16, HAS_BIAS, ACT>(gp, stream);
+    switch (nxb) {
+    case 2: return launch_tile<2, 2, OUT_BF16, HAS_BIAS, ACT>(gp, stream);
+    case 3: return launch_tile<3, 2, OUT_BF16, HAS_BIAS, ACT>(gp, stream);
+    default: return launch_tile<4, 2, OUT_BF16, HAS_BIAS, ACT>(gp, stream);
+    }
 }
 
 }  // namespace

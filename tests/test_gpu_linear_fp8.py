@@ -139,12 +139,12 @@ def test_scales_over_their_whole_range(m):
 # One ragged problem for every tile that exists: (m, n, act, output, tile rows, tile columns).  The last
 # row and column tiles are partial, and K is three scale blocks: the scale dword's last byte is padding.
 TILES = [(2290, 6128, "none", BF, 256, 256), (4600, 9200, "gelu_tanh", BF, 224, 256), (4600, 2288, "none", BF, 224, 192),
-         (1000, 4592, "gelu_tanh", BF, 192, 192), (333, 6128, "none", BF, 128, 128), (129, 4592, "none", BF, 64, 128),
+         (1000, 4592, "gelu_tanh", BF, 192, 192), (300, 9200, "none", BF, 128, 128), (333, 6128, "none", BF, 96, 128), (129, 4592, "none", BF, 64, 128),
          (4600, 4592, "swiglu", BF, 224, 128), (4090, 2032, "swiglu", BF, 256, 128), (4600, 2288, "swiglu", BF, 192, 128),
-         (333, 4592, "swiglu", BF, 128, 64), (129, 2288, "swiglu", BF, 64, 64), (2290, 6128, "none", F32, 256, 256),
-         (4600, 9200, "gelu_tanh", F32, 224, 256), (1000, 4592, "none", F32, 192, 192), (333, 6128, "gelu_tanh", F32, 128, 128),
+         (300, 4592, "swiglu", BF, 128, 64), (333, 3056, "swiglu", BF, 96, 64), (129, 2288, "swiglu", BF, 64, 64), (2290, 6128, "none", F32, 256, 256),
+         (4600, 9200, "gelu_tanh", F32, 224, 256), (1000, 4592, "none", F32, 192, 192), (300, 9200, "gelu_tanh", F32, 128, 128), (333, 6128, "none", F32, 96, 128),
          (129, 4592, "none", F32, 64, 128), (4600, 4592, "swiglu", F32, 224, 128), (4090, 2032, "swiglu", F32, 256, 128),
-         (333, 4592, "swiglu", F32, 128, 64), (129, 2288, "swiglu", F32, 64, 64)]
+         (300, 4592, "swiglu", F32, 128, 64), (333, 3056, "swiglu", F32, 96, 64), (129, 2288, "swiglu", F32, 64, 64)]
 
 
 @pytest.mark.parametrize("m,n,act,out,rows,cols", TILES)
