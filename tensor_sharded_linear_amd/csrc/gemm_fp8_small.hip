@@ -1,4 +1,13 @@
-// gemm_fp8_small.hip -- tiled product of quantized rows for a few hundred rows, eight waves.
+// gemm_fp8_small.hip -- tiled product of quantized rows for a few hundred rows, eight waves a tile.
+//
+// Between the split-K kernel's 96 rows and the thousand or so that fill the CUs with the four-wave
+// tiles, a launch is one partial round of tiles and its time is that of one tile: k-tiles times the
+// latency and the feed of one CU.  So tiles are 128, 96 or 64 rows by 128 columns, four or five k-tiles are
+// in flight in LDS, and two waves per SIMD cover each other: 8 waves in a 2 x 4 grid, scheduled
+// by the compiler within a k-tile, whose codes and scales are read from LDS a k-tile ahead.  333 x
+// 6144 x 4608 takes 21 us with bf16 output (8-bit products) and 33 with fp32 output (exact products,
+// widened to bf16); the four-wave 192 x 192 tiles take 34 and 54.  Loads alone take 0.5 to 0.7 us a
+// k-tile and CU (46 GB/s a CU), the exact products 0.4 to 0.7.
 #include "gemm_tile.h"
 #include "tp_block_internal.h"
 

@@ -1,4 +1,34 @@
-// gemm_fp8_tiled.hip -- tiled product of quantized rows on the 8-bit matrix cores, bf16 output.
+// gemm_fp8_tiled.hip -- tiled product of quantized rows for many rows, four waves a tile.
+//
+//   y[m, n] = sum_b 2^(sx[m,b] + sw[n,b]) sum_{k in block b} x[m,k] w[n,k]
+//
+// Two main loops over the same LDS tiles:
+//
+//  * mainloop8 (bf16 output): v_mfma_scale_f32_16x16x128_f8f6f4, whose 128 features are one scale block, so
+//    the matrix core multiplies by both rows' scales itself and the loop holds nothing but
+//    MFMAs, fragment reads and loads.  Among the products of each 8 consecutive features that
+//    instruction drops what lies 2^13 below the largest (found by products of chosen magnitudes), about
+//    1.5e-5 of a result: a hundredth of the bf16 rounding, but 200 times an fp32 accumulation's error.
+//  * mainloop_exact (fp32 output): the codes are widened to bf16 times their scale, which is exact,
+//    and multiplied by v_mfma_f32_16x16x32_bf16 at half the rate.
+//
+// Bound by the matrix cores.  4608 x 9216 x 6144 takes 184 us (2.83 PF; 196 with bias and GELU), where the
+// vendor library's e4m3 product with one scale per tensor takes 188; 8192^3 369 us (2.98 PF).  fp32
+// output: 4608 x 6144 x 4608 takes 174 us (1.50 PF; the vendor's bf16 product 169).  The matrix cores are
+// busy 55 to 65% of a launch's cycles; the rest is the start and the epilogue of each tile (about 8 us of
+// 62), the last round's gap, and loads that land late.
+//
+//  * 256 threads = 4 waves in a 2 x 2 grid, one wave per SIMD with 512 registers, each owning up to
+//    128 x 128 outputs as 8 x 8 accumulators in the accumulation registers; 256, 224 or 192 rows by 256 or
+//    192 columns.  MFMAs are written as assembly with their accumulators tied to those registers,
+//    and the order of every instruction between them is written out (each()).
+//  * An LDS row is the 128 bytes of one scale block of one row, so a k-tile is as many bytes as in the
+//    bf16 kernel and the MFMAs of a k-tile take as many cycles.  X fragments are read a k-tile
+//    ahead into a second set of registers, W fragments a block ahead; one barrier per k-tile, before its
+//    last W block.
+//  * Scales are loaded to LDS four k-tiles at a time (a dword a row) and read once per four k-tiles; the
+//    MFMA picks the byte by an immediate, so the loop is unrolled by four.  Reading the byte itself
+//    from LDS as an unaligned dword cost 40% (308 us for 4608 x 9216 x 6144 with GELU against 223).
 #include "gemm_tile.h"
 #include "tp_block_internal.h"
 
@@ -136,13 +166,12 @@ struct Feed {
     }
 };
 
-__device__ __forceinline__ uint32_t lds_address(const char *p)
+// An offset that the compiler cannot see through, so that it keeps this one value rather than an
+// address for every block and stage that it is added to.
+__device__ __forceinline__ int opaque(int v)
 {
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
-}
-__device__ __forceinline__ i32x4 lds_read16(uint32_t at)
-{
-    return *(__attribute__((address_space(3))) const i32x4 *)at;
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 // acc += X[m0 .., :] . W[n0 .., :]^T on the 8-bit matrix cores.
@@ -172,17 +201,17 @@ __device__ __forceinline__ void mainloop8(const Fp8Params &p, char *lds, const C
     // features these are does not matter, as both operands take the same ones.
     const int g = c.lane >> 4, swz = (c.lane >> 1) & 7;
     const int c0 = (g ^ swz) * 16, c1 = ((4 + g) ^ swz) * 16;
-    // the lane's first chunks in a tile of a stage; opaque, or the compiler keeps an address a block
+    // the lane's first chunks in a tile of a stage
     struct At {
-        uint32_t half[2];
+        const char *half[2];
     };
     auto at = [&](const char *t, int stage, int bytes) {
-        At a{{lds_address(t) + stage * bytes + c0, lds_address(t) + stage * bytes + c1}};
-        if constexpr (S > 2)
-            asm volatile("" : "+v"(a.half[0]), "+v"(a.half[1]));
-        return a;
+        const int o = stage * bytes;
+        return S > 2 ? At{{t + opaque(o + c0), t + opaque(o + c1)}} : At{{t + o + c0, t + o + c1}};
     };
-    auto read = [&](const At &a, int block, int half) { return lds_read16(a.half[half] + block * 16 * kRow); };
+    auto read = [&](const At &a, int block, int half) {
+        return *reinterpret_cast<const i32x4 *>(a.half[half] + block * 16 * kRow);
+    };
     auto set = [](i32x8 &f, int half, i32x4 v) {
         if (half == 0)
             f = __builtin_shufflevector(__builtin_shufflevector(v, v, 0, 1, 2, 3, 0, 1, 2, 3), f, 0, 1, 2, 3, 12, 13, 14, 15);
@@ -485,7 +514,9 @@ void gemm_fp8_nt_kernel(Fp8Params p)
 {
     constexpr bool kGated = ACT == kActSwiglu;
     constexpr int BM = 32 * NXB, BN = 32 * NWB, kTileCols = kGated ? BN / 2 : BN;
-    // three stages where they fit in the 160 KiB of LDS (224 x 192 and 192 x 192)
+    // Three stages where they fit in the 160 KiB of LDS (224 x 192 and 192 x 192: 512 x 9216 x 6144 in
+    // 192 x 192 takes 46 us against 60 with two).  The exact products take twice as long to cover a
+    // k-tile's loads, and gain nothing (1024 x 4608 x 6144 in 192 x 192: 73 us against 70).
     constexpr int S = !EXACT && Feed<NXB, NWB, kGated, 3>::kLdsBytes <= 160 * 1024 ? 3 : 2;
     __shared__ __attribute__((aligned(1024))) char lds[Feed<NXB, NWB, kGated, S>::kLdsBytes];
     Ctx c;
