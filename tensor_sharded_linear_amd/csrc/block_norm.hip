@@ -7,9 +7,10 @@
 // written once.  4608 x 6144 with four fp32 partials, bias, gate, modulation and quantized z takes
 // 113 us: 5.3 TB/s of 595 MB, where a large copy reaches 5.05 TB/s.  A row belongs to one workgroup of
 // 1 to 16 waves; a lane owns U units of 8 consecutive features (16 bytes of bf16), so a
-// 128-feature scale block of a quantized z is 16 neighbouring lanes.  The variance is taken about the mean from the registers (two passes over
-// registers, none over memory), so it does not cancel.  All sums are fp32: partial sums of a lane,
-// then lanes of a wave by DPP, then waves through LDS, the same order on every call.
+// 128-feature scale block of a quantized z is 16 neighbouring lanes.  The variance is taken about
+// the mean from the registers (two passes over registers, none over memory), so it does not cancel.
+// All sums are fp32: partial sums of a lane, then lanes of a wave by DPP, then waves through LDS,
+// the same order on every call.
 #include "tp_block_internal.h"
 
 namespace tpl {
