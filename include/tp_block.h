@@ -63,10 +63,10 @@ tp_status tp_quantize_fp8(const void *x, int64_t ldx, tp_dtype x_dtype, void *co
  *
  * Arithmetic: bias and activation in fp32, one rounding to y_dtype, and products and sums
  * as exact as that rounding asks for.  fp32 output, and up to 96 rows: the codes are widened
- * to bf16 (exact) and multiplied exactly, fp32 accumulation.  bf16 output of more rows: the 8-bit
- * matrix cores, which accumulate in fp32 but drop, among the products of each 8 consecutive
- * features, what lies 2^13 and more below the largest of them (about 2e-5 of the result, a hundredth of
- * the bf16 rounding).
+ * to bf16 (exact) and multiplied exactly, fp32 accumulation.  bf16 output of more rows: where the
+ * output is large, the 8-bit matrix cores, which accumulate in fp32 but drop, among the products of
+ * each 8 consecutive features, what lies 2^13 and more below the largest of them (about 2e-5 of the
+ * result, a hundredth of the bf16 rounding).
  * Requires K % 128 == 0 (the padded K of the quantized rows), n_shard % 16 == 0;
  * code pointers 16-byte aligned and their strides multiples of 16; scale pointers
  * 4-byte aligned and their strides multiples of 4 (>= K/128; the product may read,
@@ -94,9 +94,10 @@ tp_status tp_linear_rowwise_fp8(const void *x, int64_t ldx, const void *x_scale,
  * tp_linear_fp8_tile_shape -- host-only query of how the two products above run a problem of this
  * shape (K input features; for TP_ACT_SWIGLU, N counts the outputs) on the current device:
  * *tile_rows and *tile_cols receive the output tile of the tiled kernels (rows 256, 224, 192, 128, 96
- * or 64; columns 256, 192 or 128, half of that with SwiGLU), or, up to 96 rows, where the split-K
- * kernel runs, the rows that its instance holds (a multiple of 16) and the run of output columns (4 to
- * 48, at most 32 with SwiGLU) that each workgroup owns.
+ * or 64; columns 256, 192 or 128, half of that with SwiGLU), or, where the split-K kernel runs (up to
+ * 96 rows, and beyond when one round of its workgroups covers the output), the rows that a workgroup holds
+ * (a multiple of 16, up to 96) and the run of output columns (4 to 48, at most 32 with SwiGLU) that
+ * it owns.
  * Errors: TP_ERR_INVALID_ARG for a null output pointer, an unknown act or y_dtype, or sizes
  * outside 0 <= M, 0 < N, 0 < K, all at most 2^30.
  */

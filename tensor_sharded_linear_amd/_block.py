@@ -179,7 +179,7 @@ def tp_linear_colwise_fp8(x: torch.Tensor, x_scale: torch.Tensor, w_shard: torch
                           out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
                           stream=None) -> torch.Tensor:
     """Colwise shard of quantized rows: ``out = act(x @ w_shard.T + bias)``, fp32 accumulation
-    (fp32 output: exact products; bf16 output of more than 96 rows: the 8-bit matrix cores).
+    (fp32 output: exact products; large bf16 outputs of more than 96 rows: the 8-bit matrix cores).
 
     ``x``/``x_scale`` and ``w_shard``/``w_scale`` as :func:`tp_quantize_fp8` gives them; ``act``,
     ``bias`` and ``out`` as :func:`tp_linear_colwise` (``"swiglu"``: a packed [gate; up] shard)."""
@@ -225,8 +225,8 @@ def tp_linear_rowwise_fp8(x_shard: torch.Tensor, x_scale: torch.Tensor, w_shard:
 def tp_linear_fp8_tile_shape(m: int, n: int, k: int, act: str = "none",
                              out_dtype: torch.dtype = torch.bfloat16) -> tuple:
     """(rows, cols) of the output tile that the products of quantized rows use for an [m, k] x
-    [n, k]^T problem on the current device; up to 96 rows the rows that the split-K kernel's instance
-    holds and the output columns of each workgroup.  For ``act="swiglu"`` n counts the outputs.
+    [n, k]^T problem on the current device; where the split-K kernel runs (up to 96 rows, and small
+    outputs) the rows that a workgroup's instance holds and its output columns.  For ``act="swiglu"`` n counts the outputs.
     Host-only query: no device work."""
     if act not in _ACTS:
         raise ValueError("act must be 'none', 'gelu_tanh' or 'swiglu'")

@@ -3,14 +3,14 @@
 //
 //   y[m, n] = sum_b 2^(sx[m,b] + sw[n,b]) sum_{k in block b} x[m,k] w[n,k]
 //
-// Few rows take the split-K kernel (gemm_fp8_narrow.hip), a few hundred rows the eight-wave tiles
-// (gemm_fp8_small.hip), more the four-wave tiles (gemm_fp8_tiled.hip).
+// Few rows or few outputs take the split-K kernel (gemm_fp8_narrow.hip), a few hundred rows the
+// eight-wave tiles (gemm_fp8_small.hip), more the four-wave tiles (gemm_fp8_tiled.hip).
 #include "tp_block_internal.h"
 
 namespace tpl {
 namespace {
 
-// Tiles for more than kFp8NarrowMaxM rows: the candidate with the least
+// Tiles for what the split-K kernel leaves: the candidate with the least
 // (0.2 r + 0.8 ceil r) x (time of one round), r = rounds of tiles over the CUs, at least 1 (a partly
 // filled last round runs a little faster than a full one).  The times are those of K = 6144 in us,
 // between a lone round with its weights in HBM and full rounds; the choice was checked against sweeps of
@@ -60,7 +60,7 @@ TileChoice pick_tile(const Fp8Problem &p)
 
 void gemm_fp8_tile_shape(const Fp8Problem &p, int *rows, int *cols)
 {
-    if (p.M <= kFp8NarrowMaxM) {
+    if (gemm_fp8_narrow_takes(p)) {
         gemm_fp8_narrow_shape(p, rows, cols);
         return;
     }
@@ -71,11 +71,10 @@ void gemm_fp8_tile_shape(const Fp8Problem &p, int *rows, int *cols)
 
 hipError_t launch_gemm_fp8(const Fp8Problem &p, hipStream_t stream)
 {
-    if (p.M > kFp8NarrowMaxM) {
-        const TileChoice c = pick_tile(p);
-        return c.nwb == 2 ? launch_gemm_fp8_small(p, c.nxb, stream) : launch_gemm_fp8_tiled(p, c.nxb, c.nwb, stream);
-    }
-    return launch_gemm_fp8_narrow(p, stream);
+    if (gemm_fp8_narrow_takes(p))
+        return launch_gemm_fp8_narrow(p, stream);
+    const TileChoice c = pick_tile(p);
+    return c.nwb == 2 ? launch_gemm_fp8_small(p, c.nxb, stream) : launch_gemm_fp8_tiled(p, c.nxb, c.nwb, stream);
 }
 
 }  // namespace tpl

@@ -1,4 +1,4 @@
-// gemm_fp8_narrow.hip -- product of quantized rows for few rows (up to 96): split-K, exact products.
+// gemm_fp8_narrow.hip -- product of quantized rows for few rows or few outputs: split-K, exact products.
 //
 // With few rows the weight stream sets the time: 9216 x 6144 codes and their scales are 57 MB, 7 us at
 // 8 TB/s.  So a workgroup of 4 waves owns all M rows or a chunk of them, as MB blocks of 16, and a run
@@ -257,29 +257,36 @@ hipError_t launch_nb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
 
 // Output columns and activation rows per workgroup.  Every workgroup streams its weight rows (from
 // HBM) and its activation rows (from L2, like weight rows that another workgroup reads too) through one
-// CU, and the LDS ring leaves room for one workgroup per CU: the cost of a choice is ceil(workgroups / CUs)
-// x (weight rows + 0.8 x activation rows).  One chunk of rows up to a few dozen; 77 x 4608 x 6144 takes
-// two chunks of 39 rows by 36 columns (256 workgroups: 15.9 us against 17.8 for 231 of all rows by 20).
-// Ties go to fewer chunks, then to more columns.
+// CU, and the LDS ring leaves room for one workgroup per CU.  The cost of a choice is ceil(workgroups / CUs) x
+// (32 + weight rows + 0.8 x activation rows): 32 for a round's start and end; activation rows are
+// counted in whole blocks of 16, a partial block of weight rows as if half of what it lacks were there
+// (rows past the end repeat the last one, which loads cheaply).  That chooses all rows together with few
+// rows and many columns, 16 rows each with few columns, and between them what evens the CUs' loads: 77 x
+// 4608 x 6144 takes two chunks of 39 rows by 36 columns (256 workgroups: 15.9 us against 17.8 for 231 of all
+// rows by 20), 100 x 64 x 9216 seven of 15 by 4 (7.6 us against 8.8 in 32 by 16 and 18 in 96 by 16).  Ties go
+// to fewer chunks, then to more columns.
 struct Runs {
     int cols, m_rows;
+    bool one_round;
+    double cost;  // per round, without its start and end
 };
 
 Runs pick_runs(const Fp8Problem &p, int cus)
 {
-    Runs best{4, (int)p.M};
+    Runs best{4, 16, false, 0};
     double best_cost = -1;
-    for (int chunks = 1; chunks <= 4; ++chunks) {
-        const int m_rows = (int)((p.M + chunks - 1) / chunks);
-        if (chunks > 1 && m_rows < 16)
-            break;
+    const uint32_t M = p.M ? (uint32_t)p.M : 1, N = (uint32_t)p.N;
+    for (uint32_t blocks = 6; blocks >= 1; --blocks) {
+        const uint32_t chunks = (M + 16 * blocks - 1) / (16 * blocks), m_rows = (M + chunks - 1) / chunks;
         // MB + NB <= 9 blocks fit the ring: three, or with SwiGLU, which pairs them, four up to 80 rows
-        const int max_cols = p.swiglu ? (m_rows <= 80 ? 32 : 16) : 48;
-        for (int cols = max_cols; cols >= 4; cols -= 4) {
-            const int64_t wgs = (p.N + cols - 1) / cols * ((p.M + m_rows - 1) / m_rows);
-            const double cost = (double)((wgs + cus - 1) / cus) * ((p.swiglu ? 2 : 1) * cols + 0.8 * m_rows);
+        const uint32_t max_cols = p.swiglu ? (m_rows <= 80 ? 32 : 16) : 48;
+        for (uint32_t cols = max_cols; cols >= 4; cols -= 4) {
+            const uint64_t wgs = (uint64_t)((N + cols - 1) / cols) * chunks;
+            const uint32_t c16 = (cols + 15) / 16 * 16, m16 = (m_rows + 15) / 16 * 16;
+            const double one = (p.swiglu ? 1.0 : 0.5) * (cols + c16) + 0.8 * m16;
+            const double cost = (double)((wgs + cus - 1) / cus) * (one + 32);
             if (best_cost < 0 || cost < best_cost) {
-                best = Runs{cols, m_rows};
+                best = Runs{(int)cols, (int)m_rows, wgs <= (uint64_t)cus, one};
                 best_cost = cost;
             }
         }
@@ -288,6 +295,23 @@ Runs pick_runs(const Fp8Problem &p, int cus)
 }
 
 }  // namespace
+
+// Up to kFp8NarrowMaxM rows this kernel runs every product.  Beyond, it runs those whose outputs are few
+// enough for one round of workgroups, where the tiled kernels leave most CUs idle and do not split K
+// (500 x 256 x 9216: 10 us against 25 bf16 and 44 fp32 in the tile of 64 x 128; 1500 x 64 x 768: 4.4 against 5.1
+// and 6.7).  Its round takes about 2.3 + 0.13 K' + (0.027 + 0.012 K') cost us at K = 1000 K', that tile's 3.3 + 2.3
+// K' with 8-bit products and 3.4 + 4.3 K' with exact ones: with bf16 output a short K is for the tile
+// (333 x 2304 x 768: 5.7 us against 7.1; at K = 9216 28 against 22.4).
+bool gemm_fp8_narrow_takes(const Fp8Problem &p)
+{
+    if (p.M <= kFp8NarrowMaxM)
+        return true;
+    const int cus = cu_count();
+    if (p.M * p.N > (int64_t)cus * 96 * 48)
+        return false;  // more than one round whatever the choice
+    const Runs r = pick_runs(p, cus);
+    return r.one_round && (!p.out_bf16 || r.cost <= 64.0 + (double)p.K / 64);
+}
 
 void gemm_fp8_narrow_shape(const Fp8Problem &p, int *rows, int *cols)
 {

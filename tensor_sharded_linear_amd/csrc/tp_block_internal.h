@@ -83,6 +83,7 @@ void gemm_fp8_tile_shape(const Fp8Problem &p, int *rows, int *cols);
 // Up to this many rows the kernel for few rows runs.
 constexpr int64_t kFp8NarrowMaxM = 96;
 hipError_t launch_gemm_fp8_narrow(const Fp8Problem &p, hipStream_t stream);
+bool gemm_fp8_narrow_takes(const Fp8Problem &p);
 void gemm_fp8_narrow_shape(const Fp8Problem &p, int *rows, int *cols);  // of a workgroup
 // Four-wave tiles of 32 nxb x 32 nwb; eight-wave tiles of 32 nxb x 128.
 hipError_t launch_gemm_fp8_tiled(const Fp8Problem &p, int nxb, int nwb, hipStream_t stream);

@@ -99,6 +99,12 @@ def test_colwise_refusals():
 def test_tile_shape_query():
     assert tsl.tp_linear_fp8_tile_shape(1, 9216, 6144) == (16, 36)
     assert tsl.tp_linear_fp8_tile_shape(96, 9216, 6144, "none", torch.float32) == (96, 36)
+    assert tsl.tp_linear_fp8_tile_shape(0, 64, 128)[1] in range(4, 49)
+    # one round of the split-K kernel's workgroups covers a small output, whatever its rows
+    for out in (torch.bfloat16, torch.float32):
+        rows, cols = tsl.tp_linear_fp8_tile_shape(500, 256, 9216, "none", out)
+        assert rows in (16, 32, 48) and cols in (16, 32, 48)
+    assert tsl.tp_linear_fp8_tile_shape(1 << 30, 1 << 30, 128) == (256, 256)
     rows, cols = tsl.tp_linear_fp8_tile_shape(4608, 9216, 6144, "gelu_tanh")
     assert rows in (192, 224, 256) and cols in (192, 256)
     for bad in (dict(m=-1), dict(n=0), dict(k=0), dict(k=1 << 31), dict(act="relu"), dict(out_dtype=torch.float16)):

@@ -60,7 +60,8 @@ def test_epilogues_within_the_derived_bound(m, act, bias, out):
 
 
 @pytest.mark.parametrize("m,n,k", [(700, 1040, 2304), (1500, 2320, 768), (4608, 272, 128), (90, 4624, 512),
-                                   (1, 9232, 6144), (2, 16, 18432)])
+                                   (1, 9232, 6144), (2, 16, 18432), (97, 9216, 256), (500, 256, 4608),
+                                   (1500, 64, 896), (75001, 16, 384), (18999, 64, 256)])
 def test_many_tiles(m, n, k):
     g = torch.Generator().manual_seed(m + n + k)
     x, w = _integers(g, m, k), _integers(g, n, k)
@@ -70,7 +71,7 @@ def test_many_tiles(m, n, k):
     assert torch.equal(tsl.tp_linear_colwise_fp8(*x, *w), want.float().to(BF))
 
 
-@pytest.mark.parametrize("m", [3, 60, 300])
+@pytest.mark.parametrize("m", [3, 60, 300, 13000])
 @pytest.mark.parametrize("act", ["none", "swiglu"])
 def test_strided_operands_and_outputs(m, act):
     """Operands are columns [512, 1280) of wider rows (scale columns [4, 10)), the output lies inside a
@@ -89,7 +90,24 @@ def test_strided_operands_and_outputs(m, act):
         assert (buf == 7).all()
 
 
-@pytest.mark.parametrize("m", [1, 20, 100, 260])
+@pytest.mark.parametrize("m,n,out,rows,cols", [(2290, 6128, BF, 256, 256), (4600, 2288, BF, 224, 192), (1000, 4592, BF, 192, 192),
+                                                (2290, 6128, F32, 256, 256), (4600, 9200, F32, 224, 256),
+                                                (1000, 4592, F32, 192, 192)])
+def test_strided_operands_of_the_large_tiles(m, n, out, rows, cols):
+    assert tsl.tp_linear_fp8_tile_shape(m, n, 640, "none", out) == (rows, cols)
+    g = torch.Generator().manual_seed(rows)
+    xc, xs = _integers(g, m, 1536)
+    wc, ws = _integers(g, n, 1536)
+    x, w = (xc[:, 512:1152], xs[:, 4:9]), (wc[:, 512:1152], ws[:, 4:9])
+    buf = torch.full((m + 2, n + 32), 7.0, dtype=out, device="cuda")
+    y = tsl.tp_linear_colwise_fp8(*x, *w, out=buf[1:m + 1, 16:16 + n])
+    want = ref.values(*x).cuda() @ ref.values(*w).cuda().t().contiguous()
+    assert torch.equal(y, want.to(out))
+    buf[1:m + 1, 16:16 + n] = 7.0
+    assert (buf == 7).all()
+
+
+@pytest.mark.parametrize("m", [1, 20, 100, 260, 8400])
 def test_nan_blocks_reach_their_row_and_column_only(m):
     """A NaN scale in one activation row and one weight row makes that output row and column NaN."""
     g = torch.Generator().manual_seed(m)
@@ -105,7 +123,7 @@ def test_nan_blocks_reach_their_row_and_column_only(m):
     assert torch.equal(torch.isnan(y), want)
 
 
-@pytest.mark.parametrize("m", [1, 20, 100, 260])
+@pytest.mark.parametrize("m", [1, 20, 100, 260, 25000])
 @pytest.mark.parametrize("out", [BF, F32])
 def test_nan_scales_of_finite_codes(m, out):
     """A scale byte of 255 is NaN whatever the codes: one block of a row of each operand."""
@@ -122,7 +140,7 @@ def test_nan_scales_of_finite_codes(m, out):
     assert torch.equal(torch.isnan(y), want)
 
 
-@pytest.mark.parametrize("m", [1, 40, 300])
+@pytest.mark.parametrize("m", [1, 40, 300, 19000])
 def test_scales_over_their_whole_range(m):
     """Scales 2^-60 .. 2^60 whose products stay within fp32: the scale of each block counts."""
     g = torch.Generator().manual_seed(5)
@@ -139,12 +157,12 @@ def test_scales_over_their_whole_range(m):
 # One ragged problem for every tile that exists: (m, n, act, output, tile rows, tile columns).  The last
 # row and column tiles are partial, and K is three scale blocks: the scale dword's last byte is padding.
 TILES = [(2290, 6128, "none", BF, 256, 256), (4600, 9200, "gelu_tanh", BF, 224, 256), (4600, 2288, "none", BF, 224, 192),
-         (1000, 4592, "gelu_tanh", BF, 192, 192), (300, 9200, "none", BF, 128, 128), (333, 6128, "none", BF, 96, 128), (129, 4592, "none", BF, 64, 128),
+         (1000, 4592, "gelu_tanh", BF, 192, 192), (300, 9200, "none", BF, 128, 128), (333, 6128, "none", BF, 96, 128), (129, 9200, "none", BF, 64, 128),
          (4600, 4592, "swiglu", BF, 224, 128), (4090, 2032, "swiglu", BF, 256, 128), (4600, 2288, "swiglu", BF, 192, 128),
-         (300, 4592, "swiglu", BF, 128, 64), (333, 3056, "swiglu", BF, 96, 64), (129, 2288, "swiglu", BF, 64, 64), (2290, 6128, "none", F32, 256, 256),
+         (300, 4592, "swiglu", BF, 128, 64), (333, 3056, "swiglu", BF, 96, 64), (129, 4592, "swiglu", BF, 64, 64), (2290, 6128, "none", F32, 256, 256),
          (4600, 9200, "gelu_tanh", F32, 224, 256), (1000, 4592, "none", F32, 192, 192), (300, 9200, "gelu_tanh", F32, 128, 128), (333, 6128, "none", F32, 96, 128),
-         (129, 4592, "none", F32, 64, 128), (4600, 4592, "swiglu", F32, 224, 128), (4090, 2032, "swiglu", F32, 256, 128),
-         (300, 4592, "swiglu", F32, 128, 64), (333, 3056, "swiglu", F32, 96, 64), (129, 2288, "swiglu", F32, 64, 64)]
+         (129, 9200, "none", F32, 64, 128), (4600, 4592, "swiglu", F32, 224, 128), (4090, 2032, "swiglu", F32, 256, 128),
+         (300, 4592, "swiglu", F32, 128, 64), (333, 3056, "swiglu", F32, 96, 64), (129, 4592, "swiglu", F32, 64, 64)]
 
 
 @pytest.mark.parametrize("m,n,act,out,rows,cols", TILES)
