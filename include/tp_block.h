@@ -14,7 +14,9 @@
  *                       codes past K are zero;
  *   scales  [rows, K8 / 128]  e8m0, one byte each: byte s stands for
  *                       2^(s - 127), 255 for NaN.
- * Feature k of row r stands for codes[r, k] * 2^(scales[r, k / 128] - 127).
+ * Feature k of row r stands for codes[r, k] * 2^(scales[r, k / 128] - 127).  The products keep the
+ * values that fp32 holds as normal numbers, 2^-126 to below 2^128; smaller ones may count as zero,
+ * larger ones as infinite.
  * Scales are powers of two: the CDNA4 matrix cores apply them inside the
  * product, and scaling by one is exact.  Both operands of a product carry a
  * scale for each 128 features of each row, so a shard of quantized rows is cut
@@ -34,8 +36,7 @@ extern "C" {
  * tp_quantize_fp8 -- rows of x to codes and scales.
  *
  *   x       [M, K]        bf16 or fp32 (x_dtype), row stride ldx >= K elements;
- *                         element alignment suffices (16-byte aligned base and
- *                         rows take the faster path)
+ *                         element alignment suffices
  *   codes   [M, K8]       row stride ldc >= K8 bytes, base and ldc multiples of 16
  *   scales  [M, K8/128]   row stride lds >= K8/128 bytes, base and lds multiples of 4;
  *                         bytes past K8/128 are not written
@@ -128,8 +129,8 @@ tp_status tp_linear_fp8_tile_shape(int64_t M, int64_t N, int64_t K, tp_act act, 
  * values.  A gate, scale or shift that is NULL does not take part (1, 0, 0).
  *
  * Aliasing: h may be x (same pointer, stride and dtype).  Otherwise outputs overlap
- * nothing.  Element alignment suffices for every input, h and z; rows that all start
- * at 16-byte addresses take the faster path.  Quantized z: as tp_quantize_fp8's outputs.
+ * nothing.  Element alignment suffices for every input, h and z.  Quantized z: as
+ * tp_quantize_fp8's outputs.
  * D at most 32768 (TP_ERR_UNSUPPORTED above), num_parts at most 16.
  */
 typedef enum { TP_NORM_NONE = 0, TP_NORM_LAYER = 1, TP_NORM_RMS = 2 } tp_norm;

@@ -6,7 +6,8 @@ every step of the computation runs in the HIP kernels behind the C ABI.
 
 Quantized rows are a pair ``(codes, scales)``: codes ``[rows, K8]`` ``torch.float8_e4m3fn`` with
 K8 = K rounded up to a multiple of 128 (zero codes past K), scales ``[rows, K8 / 128]``
-``torch.float8_e8m0fnu`` (powers of two).
+``torch.float8_e8m0fnu`` (powers of two).  Scale rows start at whole dwords: their row stride is a
+multiple of 4, as :func:`tp_quantize_fp8` lays them out.
 """
 from __future__ import annotations
 

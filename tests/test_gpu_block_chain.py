@@ -43,7 +43,7 @@ def _chain(x, w, stream=None, keep=None):
     return tsl.tp_block_norm(x, parts, bias=w["b2"], gate=mod[2], scale=mod[3], shift=mod[4], group_rows=m, stream=stream)
 
 
-@pytest.mark.parametrize("m", [1, 7, 64, 200, 700])
+@pytest.mark.parametrize("m", [1, 7, 64, 200, 700, 3001])
 def test_chain_step_by_step(m):
     w = _weights(m)
     x = torch.randn(m, D, generator=torch.Generator().manual_seed(m)).to(BF).cuda()
@@ -59,7 +59,7 @@ def test_chain_step_by_step(m):
     ref.check(z, wz, ez)
 
 
-@pytest.mark.parametrize("m", [5, 300])
+@pytest.mark.parametrize("m", [5, 300, 3001])
 def test_graph_replays_equal_eager(m):
     """Replays with eager work and synchronisations between them, each against the eager result."""
     w = _weights(1)
@@ -87,7 +87,7 @@ def test_graph_replays_equal_eager(m):
 def test_another_stream_and_threads():
     """Each thread on its own stream (given explicitly, not current): the same bits as alone."""
     ws = [_weights(s) for s in range(3)]
-    xs = [torch.randn(m, D, generator=torch.Generator().manual_seed(m)).to(BF).cuda() for m in (3, 120, 260)]
+    xs = [torch.randn(m, D, generator=torch.Generator().manual_seed(m)).to(BF).cuda() for m in (3, 120, 2500)]
     want = [_chain(x, w) for x, w in zip(xs, ws)]
     torch.cuda.synchronize()
     got, bad = [None] * 3, []

@@ -54,7 +54,7 @@ def _run(m, d, *, x=BF, parts=0, part=F32, bias=False, post="none", gate=False, 
 
 
 SIZES = [(1, 1), (1, 64), (3, 8), (2, 127), (5, 513), (4, 520), (9, 1536), (3, 2309), (2, 4104), (2, 6144), (1, 9000),
-         (2, 16384), (1, 32768), (300, 264), (1025, 72)]
+         (2, 16384), (2, 20011), (1, 24576), (1, 32768), (300, 264), (1025, 72), (520, 4616)]
 
 
 @pytest.mark.parametrize("m,d", SIZES)
@@ -159,6 +159,29 @@ def test_strided_tables_rows_and_outputs():
     hb[:, 3:3 + d] = 5
     zb[:, 5:5 + d] = 5
     assert (hb == 5).all() and (zb == 5).all()
+
+
+def test_more_rows_than_one_launch_and_offsets_beyond_32_bits():
+    """2^21 + 77 short rows (two launches), and rows that lie 2^30 and more elements apart."""
+    g = torch.Generator("cuda").manual_seed(6)
+    x = torch.randn((1 << 21) + 77, 8, generator=g, device="cuda")
+    p = torch.randn(x.shape, generator=g, device="cuda")
+    index = torch.arange(x.shape[0], dtype=torch.int32, device="cuda") % 3
+    gate = torch.randn(3, 8, generator=g, device="cuda").to(BF)
+    h, z = tsl.tp_block_norm(x, [p], gate=gate, group_index=index, z_dtype=F32)
+    for s in (slice(0, 50), slice((1 << 21) - 50, None)):
+        (wh, eh), (wz, ez) = ref.block_norm(x[s], [p[s]], None, ("none", None, None), gate, 1.0, ("layer", None, None),
+                                            None, None, EPS, index[s].long().cpu())
+        ref.check(h[s], wh, eh)
+        ref.check(z[s], wz, ez)
+    d, ld = 640, (1 << 30) + 640
+    bufs = [torch.empty(3 * ld, dtype=BF, device="cuda").as_strided((3, d), (ld, 1)) for _ in range(3)]
+    for i, b in enumerate(bufs):
+        b.copy_(torch.randn(3, d, generator=torch.Generator().manual_seed(i)).to(BF))
+    x, p = bufs[0].clone(), bufs[1].clone()
+    h, z = tsl.tp_block_norm(bufs[0], [bufs[1]], h_out=bufs[0], z_out=bufs[2])
+    wh, wz = tsl.tp_block_norm(x, [p])
+    assert torch.equal(h, wh) and torch.equal(z, wz)
 
 
 def test_one_group_vectors_and_empty():

@@ -154,6 +154,38 @@ def test_scales_over_their_whole_range(m):
     ref.check(y, *ref.linear(ref.values(*x), ref.values(*w), None, "none"))
 
 
+@pytest.mark.parametrize("m", [1, 40, 300, 19000])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_scales_near_the_ends_of_their_range(m, out):
+    """Values of 2^-120 and 2^121 are normal numbers of the widened operands: no block is lost."""
+    g = torch.Generator().manual_seed(7)
+    n, k = 64, 512
+    xc = torch.randint(1, 5, (m, k), generator=g).float().to(torch.float8_e4m3fn)
+    wc = torch.randint(1, 5, (n, k), generator=g).float().to(torch.float8_e4m3fn)
+    e = torch.tensor([-120, 119, -100, 100])
+    x = _pair(xc, (127 + e).to(torch.uint8).expand(m, 4).contiguous())
+    w = _pair(wc, (127 - e + torch.randint(-2, 3, (n, 4), generator=g)).to(torch.uint8))
+    y = tsl.tp_linear_colwise_fp8(*x, *w, out_dtype=out)
+    ref.check(y, *ref.linear(ref.values(*x), ref.values(*w), None, "none", out == BF and m > 96))
+
+
+@pytest.mark.parametrize("m", [1, 20, 100, 260, 25000])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_nan_codes_under_finite_scales(m, out):
+    """The codes 0x7f and 0xff are NaN whatever the scale: one feature of a row of each operand."""
+    g = torch.Generator().manual_seed(m)
+    n, k = 48, 640
+    xc, wc = (torch.randn(r, k, generator=g).to(torch.float8_e4m3fn) for r in (m, n))
+    xs, ws = (torch.full((r, k // 128), 127, dtype=torch.uint8) for r in (m, n))
+    xc.view(torch.uint8)[m - 1, 333] = 0x7f
+    wc.view(torch.uint8)[11, 639] = 0xff
+    y = tsl.tp_linear_colwise_fp8(*_pair(xc, xs), *_pair(wc, ws), out_dtype=out).cpu()
+    want = torch.zeros(m, n, dtype=torch.bool)
+    want[m - 1] = True
+    want[:, 11] = True
+    assert torch.equal(torch.isnan(y), want)
+
+
 # One ragged problem for every tile that exists: (m, n, act, output, tile rows, tile columns).  The last
 # row and column tiles are partial, and K is three scale blocks: the scale dword's last byte is padding.
 TILES = [(2290, 6128, "none", BF, 256, 256), (4600, 9200, "gelu_tanh", BF, 224, 256), (4600, 2288, "none", BF, 224, 192),
@@ -184,6 +216,18 @@ def test_every_tile_with_ragged_edges(m, n, act, out, rows, cols, k):
         want = s[:, :n] * torch.sigmoid(s[:, :n]) * s[:, n:]
     bound = 1e-5 * (1 + want.abs()) * 1.01 + ref.HALF_STEP[out] * want.abs()
     assert bool(((y - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("m,n", [(90, 128), (500, 128), (129, 9200), (1000, 4592), (2290, 6128)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_output_rows_beyond_32_bit_offsets(m, n, out):
+    """Output rows far apart: the last ones lie more than 2^32 bytes behind the first."""
+    g = torch.Generator().manual_seed(m)
+    x, w = _integers(g, m, 256), _integers(g, n, 256)
+    ld = ((1 << 32) // (m - 40) + 63) // 16 * 16
+    y = torch.empty(m * ld, dtype=out, device="cuda").as_strided((m, n), (ld, 1))
+    tsl.tp_linear_colwise_fp8(*x, *w, out=y)
+    assert torch.equal(y.contiguous(), tsl.tp_linear_colwise_fp8(*x, *w, out_dtype=out))
 
 
 def test_no_rows_is_a_no_op():
