@@ -96,12 +96,12 @@ def _same_device(x: torch.Tensor, **others: Optional[torch.Tensor]) -> None:
 
 
 def _empty_codes(m: int, k: int, device):
-    """Codes and scales for m rows of k features; scale rows padded to whole dwords."""
+    """Codes and scales for m rows of k features; scale rows start at whole dwords.  (A product reads the
+    last row's last dword whole: its last bytes may lie past the tensor, never past its allocation,
+    whose granularity is a multiple of four.)"""
     kb = -(-k // BLOCK)
-    codes = torch.empty_strided((m, kb * BLOCK), (kb * BLOCK, 1), dtype=CODES, device=device)
-    pad = -(-kb // 4) * 4
-    return codes, torch.empty((m, pad), dtype=SCALES, device=device).as_strided((m, kb), (pad, 1)) if kb % 4 else \
-        torch.empty_strided((m, kb), (kb, 1), dtype=SCALES, device=device)
+    return torch.empty_strided((m, kb * BLOCK), (kb * BLOCK, 1), dtype=CODES, device=device), \
+        torch.empty_strided((m, kb), ((kb + 3) & -4, 1), dtype=SCALES, device=device)
 
 
 def _codes(t: torch.Tensor, s: torch.Tensor, name: str, m: Optional[int] = None, k8: Optional[int] = None) -> None:
@@ -123,6 +123,32 @@ def _lds(s: torch.Tensor) -> int:
     return -(-max(s.stride(0), s.shape[1]) // 4) * 4
 
 
+def _input(x: torch.Tensor):
+    """(dtype number, device index, shape, address, row stride) of the matrix x."""
+    try:
+        shape, (ld, c) = x.shape, x.stride()
+        (m, k), dtype, index = shape, _DT.get(x.dtype), x.get_device()
+        good = dtype is not None and index >= 0 and k > 0 and (c == 1 or k == 1)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        _dev2d(x, "x")   # names what is wrong, unless the type or the width is
+        if x.dtype not in _DT:
+            raise TypeError(f"x must be bf16 or fp32, got {x.dtype}")
+        raise ValueError("x has no columns")
+    return dtype, index, shape, x.data_ptr(), ld if m > 1 else k
+
+
+def _place(t: torch.Tensor, name: str, shape, index: int):
+    """(address, row stride) of a row-major matrix of this shape on cuda:`index`."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name} must be a [{shape[0]}, {shape[1]}] tensor on cuda:{index}")
+    ld, c = t.stride()
+    if c != 1 and shape[1] > 1:
+        _dev2d(t, name)   # raises
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
 def tp_quantize_fp8(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
                     scales: Optional[torch.Tensor] = None, stream=None):
     """Quantize the rows of ``x`` [M, K] (bf16 or fp32, any K) to e4m3 codes with one
@@ -131,12 +157,7 @@ def tp_quantize_fp8(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
     Scale: the least 2^e, e >= -126, with max|x| <= 448 2^e (1 for an all-zero block); codes:
     x / 2^e rounded to nearest even.  A block with an infinity or a NaN becomes NaN."""
     lib = _library()
-    x = _dev2d(x, "x")
-    if x.dtype not in _DT:
-        raise TypeError(f"x must be bf16 or fp32, got {x.dtype}")
-    m, k = x.shape
-    if k == 0:
-        raise ValueError("x has no columns")
+    dtype, _, (m, k), address, ld = _input(x)
     if (codes is None) != (scales is None):
         raise ValueError("pass both codes and scales, or neither")
     if codes is None:
@@ -144,8 +165,8 @@ def tp_quantize_fp8(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
     else:
         _codes(codes, scales, "output", m, -(-k // BLOCK) * BLOCK)
         _same_device(x, codes=codes, scales=scales)
-    _call(lib.tp_quantize_fp8, x, stream, x.data_ptr(), _ld(x), _DT[x.dtype], codes.data_ptr(), _ld(codes),
-          scales.data_ptr(), _lds(scales), m, k)
+    _call(lib.tp_quantize_fp8, x, stream, address, ld, dtype, codes.data_ptr(), _ld(codes), scales.data_ptr(),
+          _lds(scales), m, k)
     return codes, scales
 
 
@@ -238,13 +259,21 @@ def tp_linear_fp8_tile_shape(m: int, n: int, k: int, act: str = "none",
     return rows.value, cols.value
 
 
-def _feature_vec(t: Optional[torch.Tensor], name: str, d: int, index: int) -> int:
-    if t is None:
-        return 0
-    if t.get_device() != index or t.dtype != torch.bfloat16 or t.dim() != 1 or t.numel() != d or \
-            (d > 1 and t.stride(0) != 1):
+def _feature_vec(t: torch.Tensor, name: str, d: int, index: int) -> int:
+    if t.get_device() != index or t.dtype != torch.bfloat16 or t.shape != (d,) or (d > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous bf16 vector of length {d} on cuda:{index}")
     return t.data_ptr()
+
+
+def _table(t: torch.Tensor, name: str, like: torch.Tensor, groups: int, d: int, index: int):
+    """(address, row stride) of a modulation table [groups, d], or [d] for one group."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) not in (1, 2) or shape[-1] != d or t.dtype not in _DT or t.get_device() != index or \
+            (strides[-1] != 1 and d > 1):
+        raise ValueError(f"{name} must be [groups, {d}] bf16 or fp32 on cuda:{index}, with unit column stride")
+    if t.dtype != like.dtype or (shape[0] if len(shape) == 2 else 1) != groups:
+        raise ValueError("gate, scale and shift must have one dtype and one number of groups")
+    return t.data_ptr(), strides[0] if groups > 1 else d
 
 
 def tp_block_norm(x: torch.Tensor, parts: Optional[Sequence[torch.Tensor]] = None, *,
@@ -270,99 +299,95 @@ def tp_block_norm(x: torch.Tensor, parts: Optional[Sequence[torch.Tensor]] = Non
     Returns ``(h, z)``: h of ``x``'s dtype (``h_out`` may be ``x`` itself), z of ``z_dtype`` (bf16,
     fp32, or ``torch.float8_e4m3fn`` for a ``(codes, scales)`` pair), None for ``pre_norm="none"``."""
     lib = _library()
-    x = _dev2d(x, "x")
-    if x.dtype not in _DT:
-        raise TypeError(f"x must be bf16 or fp32, got {x.dtype}")
-    m, d = x.shape
-    if d == 0:
-        raise ValueError("x has no columns")
-    if post_norm not in _NORMS or pre_norm not in _NORMS:
+    x_dt, index, shape, x_p, ldx = _input(x)
+    m, d = shape
+    post, pre = _NORMS.get(post_norm), _NORMS.get(pre_norm)
+    if post is None or pre is None:
         raise ValueError("post_norm and pre_norm must be 'none', 'layer' or 'rms'")
-    index = x.get_device()
     h, z = x, None
-    part_array, num_parts, ldp, part_dt, h_args = None, 0, 0, 0, (0, 0, 0)
+    part_array = parts_p = num_parts = ldp = part_dt = h_p = ldh = h_dt = 0
     if parts is not None:
-        parts = list(parts)
-        if not parts:
-            raise ValueError("no parts (pass None for a norm without a block's output)")
-        p0 = _dev2d(parts[0], "parts[0]")
-        ldp = _ld(p0)
-        if p0.dtype not in _DT:
-            raise TypeError(f"parts must be bf16 or fp32, got {p0.dtype}")
-        strides = p0.stride()
-        for i, p in enumerate(parts):
-            if p.shape != x.shape or p.dtype != p0.dtype or p.get_device() != index or \
-                    (p.stride() != strides and _ld(_dev2d(p, f"parts[{i}]")) != ldp):
-                raise ValueError(f"all parts must be [{m}, {d}], of one dtype and row stride, on {x.device}")
-        if h_out is None:
-            h = torch.empty_strided((m, d), (d, 1), dtype=x.dtype, device=x.device)
-        else:
-            h = _dev2d(h_out, "h_out")
-            if h.shape != x.shape or h.dtype not in _DT or h.get_device() != index:
-                raise ValueError(f"h_out must be [{m}, {d}] bf16 or fp32 on {x.device}")
         num_parts = len(parts)
-        part_array = (_P * num_parts)(*[p.data_ptr() for p in parts])
-        part_dt, h_args = _DT[p0.dtype], (h.data_ptr(), _ld(h), _DT[h.dtype])
+        if not num_parts:
+            raise ValueError("no parts (pass None for a norm without a block's output)")
+        dtype, addresses = parts[0].dtype, []
+        for i, p in enumerate(parts):
+            address, ld = _place(p, f"parts[{i}]", shape, index)
+            addresses.append(address)
+            if i == 0:
+                ldp = ld
+            if p.dtype != dtype or ld != ldp:
+                raise ValueError("all parts must be of one dtype and row stride")
+        if dtype not in _DT:
+            raise TypeError(f"parts must be bf16 or fp32, got {dtype}")
+        part_array, part_dt = (_P * num_parts)(*addresses), _DT[dtype]
+        parts_p = ctypes.addressof(part_array)
+        if h_out is None:
+            h = torch.empty_strided(shape, (d, 1), dtype=x.dtype, device=x.device)
+            h_p, ldh, h_dt = h.data_ptr(), d, x_dt
+        else:
+            h = h_out
+            h_p, ldh = _place(h, "h_out", shape, index)
+            if h.dtype not in _DT:
+                raise ValueError(f"h_out must be bf16 or fp32, got {h.dtype}")
+            h_dt = _DT[h.dtype]
     elif h_out is not None:
         raise ValueError("h_out without parts")
-    z_args, z_rows = (0, 0, 0, 0), 0
-    if pre_norm == "none":
+    z_p = ldz = zs_p = ldzs = z_rows = 0
+    if not pre:
         if z_out is not None:
             raise ValueError("z_out without pre_norm")
-    elif z_dtype == CODES:
-        if z_out is None:
-            codes, scales = z = _empty_codes(m, d, x.device)
-        else:
-            codes, scales = z = z_out
-            _codes(codes, scales, "z_out", m, -(-d // BLOCK) * BLOCK)
-            _same_device(x, z_codes=codes, z_scales=scales)
-        z_args, z_rows = (codes.data_ptr(), _ld(codes), scales.data_ptr(), _lds(scales)), _ROWS[CODES]
+    elif z_dtype not in _ROWS:
+        raise ValueError("z_dtype must be bf16, fp32 or float8_e4m3fn")
     else:
-        if z_dtype not in _ROWS:
-            raise ValueError("z_dtype must be bf16, fp32 or float8_e4m3fn")
-        if z_out is None:
-            z = torch.empty_strided((m, d), (d, 1), dtype=z_dtype, device=x.device)
+        z_rows = _ROWS[z_dtype]
+        if z_dtype == CODES:
+            if z_out is None:
+                codes, scales = z = _empty_codes(m, d, x.device)
+            else:
+                codes, scales = z = z_out
+                _codes(codes, scales, "z_out", m, -(-d // BLOCK) * BLOCK)
+                _same_device(x, z_codes=codes, z_scales=scales)
+            z_p, ldz, zs_p, ldzs = codes.data_ptr(), _ld(codes), scales.data_ptr(), _lds(scales)
+        elif z_out is None:
+            z = torch.empty_strided(shape, (d, 1), dtype=z_dtype, device=x.device)
+            z_p, ldz = z.data_ptr(), d
         else:
-            z = _dev2d(z_out, "z_out", z_dtype)
-            if z.shape != x.shape or z.get_device() != index:
-                raise ValueError(f"z_out must be [{m}, {d}] on {x.device}")
-        z_args, z_rows = (z.data_ptr(), _ld(z), 0, 0), _ROWS[z_dtype]
-    tables, first, groups = [], None, 0
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
-        if t is None:
-            tables.append((0, 0))
-            continue
-        rows, cols = t.shape if t.dim() == 2 else (1, t.numel())
-        if t.dim() not in (1, 2) or cols != d or t.dtype not in _DT or t.get_device() != index or \
-                (d > 1 and t.stride(-1) != 1):
-            raise ValueError(f"{name} must be [groups, {d}] bf16 or fp32 on {x.device}, with unit column stride")
-        if first is None:
-            first, groups = t.dtype, rows
-        elif t.dtype != first or rows != groups:
-            raise ValueError("gate, scale and shift must have one dtype and one number of groups")
-        tables.append((t.data_ptr(), t.stride(0) if rows > 1 else d))
-    mod_dt, index_ptr = 0, 0
+            z = z_out
+            z_p, ldz = _place(z, "z_out", shape, index)
+            if z.dtype != z_dtype:
+                raise TypeError(f"z_out must be {z_dtype}, got {z.dtype}")
+    mod_dt = groups = index_p = gate_p = ld_gate = scale_p = ld_scale = shift_p = ld_shift = 0
+    first = gate if gate is not None else scale if scale is not None else shift
     if first is not None:
-        mod_dt = _DT[first]
+        groups = first.shape[0] if first.dim() == 2 else 1
+        if gate is not None:
+            gate_p, ld_gate = _table(gate, "gate", first, groups, d, index)
+        if scale is not None:
+            scale_p, ld_scale = _table(scale, "scale", first, groups, d, index)
+        if shift is not None:
+            shift_p, ld_shift = _table(shift, "shift", first, groups, d, index)
+        mod_dt = _DT[first.dtype]
         if group_index is not None:
             if group_rows is not None:
                 raise ValueError("pass group_rows or group_index, not both")
-            if group_index.get_device() != index or group_index.dtype != torch.int32 or \
-                    tuple(group_index.shape) != (m,) or (m > 1 and group_index.stride(0) != 1):
-                raise ValueError(f"group_index must be a contiguous int32 vector of length {m} on {x.device}")
-            index_ptr = group_index.data_ptr()
+            if group_index.get_device() != index or group_index.dtype != torch.int32 or group_index.shape != (m,) or \
+                    (m > 1 and group_index.stride(0) != 1):
+                raise ValueError(f"group_index must be a contiguous int32 vector of length {m} on cuda:{index}")
+            index_p = group_index.data_ptr()
         elif group_rows is None:
             if groups == 0 or m % groups:
                 raise ValueError(f"{groups} groups do not divide {m} rows: pass group_rows or group_index")
             group_rows = max(1, m // groups)
     elif group_index is not None:
         raise ValueError("group_index without a gate, scale or shift")
-    (gate_p, gate_ld), (scale_p, scale_ld), (shift_p, shift_ld) = tables
-    args = _PACK.pack(
-        m, d, x.data_ptr(), _ld(x), _DT[x.dtype], part_dt, 0 if part_array is None else ctypes.addressof(part_array),
-        ldp, num_parts, _NORMS[post_norm], _feature_vec(bias, "bias", d, index), _feature_vec(post_weight, "post_weight", d, index),
-        _feature_vec(post_bias, "post_bias", d, index), *h_args, _NORMS[pre_norm], _feature_vec(pre_weight, "pre_weight", d, index),
-        _feature_vec(pre_bias, "pre_bias", d, index), *z_args, z_rows, mod_dt, gate_p, scale_p, shift_p, gate_ld, scale_ld,
-        shift_ld, groups, 0 if group_rows is None else group_rows, index_ptr, residual_scale, eps)
-    _call(lib.tp_block_norm, x, stream, args)
+    bias_p = 0 if bias is None else _feature_vec(bias, "bias", d, index)
+    post_w = 0 if post_weight is None else _feature_vec(post_weight, "post_weight", d, index)
+    post_b = 0 if post_bias is None else _feature_vec(post_bias, "post_bias", d, index)
+    pre_w = 0 if pre_weight is None else _feature_vec(pre_weight, "pre_weight", d, index)
+    pre_b = 0 if pre_bias is None else _feature_vec(pre_bias, "pre_bias", d, index)
+    args = _PACK.pack(m, d, x_p, ldx, x_dt, part_dt, parts_p, ldp, num_parts, post, bias_p, post_w, post_b, h_p, ldh, h_dt,
+                      pre, pre_w, pre_b, z_p, ldz, zs_p, ldzs, z_rows, mod_dt, gate_p, scale_p, shift_p, ld_gate,
+                      ld_scale, ld_shift, groups, group_rows or 0, index_p, residual_scale, eps)
+    _call(lib.tp_block_norm, x, stream, args)   # part_array, which args points to, lives until here
     return h, z
