@@ -161,7 +161,9 @@ __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const C
         return f32x4{(float)bb[0], (float)bb[1], (float)bb[2], (float)bb[3]};
     };
     // BIAS_AHEAD: the wave's bias values in registers before the first slice.  Loaded where they are
-    // used, each slice waits for them again, as the output's stores might change them.
+    // used, each slice waits for them again, as the output's stores might change them.  Columns past
+    // the end take the last ones' and are added like the others, without a branch (4608 x 9216 x 6144
+    // with GELU in 8-bit products: 3 us less in three rounds of tiles).
     bf16x4 bias_v[kGated ? 2 : 1][JO];
     if constexpr (HAS_BIAS && BIAS_AHEAD) {
 #pragma unroll
@@ -196,7 +198,7 @@ __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const C
         for (int j = 0; j < JO; ++j) {
             const int n = n0 + c.wave_n * WNO + j * 16 + ncol;  // N % 16 == 0: n < N covers n + 3
             f32x4 v = acc[i][j];
-            if (HAS_BIAS && n < p.N)
+            if (HAS_BIAS && (BIAS_AHEAD || n < p.N))
                 v = v + bias_of(0, j, n);
             if (ACT == kActGelu) {
                 v[0] = gelu_tanh(v[0]);
@@ -206,7 +208,7 @@ __device__ __forceinline__ void epilogue(const Params &p, uint16_t *lds, const C
             }
             if (kGated) {
                 f32x4 u = acc[i][j + NWB / 2];
-                if (HAS_BIAS && n < p.N)
+                if (HAS_BIAS && (BIAS_AHEAD || n < p.N))
                     u = u + bias_of(1, j, n);
                 v[0] = silu(v[0]) * u[0];
                 v[1] = silu(v[1]) * u[1];
