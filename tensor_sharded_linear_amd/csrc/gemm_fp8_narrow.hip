@@ -317,8 +317,8 @@ Runs pick_runs(const Fp8Problem &p, int cus)
 // enough for one round of workgroups, where the tiled kernels leave most CUs idle and do not split K
 // (500 x 256 x 9216: 10 us against 25 bf16 and 44 fp32 in the tile of 64 x 128; 1500 x 64 x 768: 4.4 against 5.1
 // and 6.7).  Its round takes about 2.3 + 0.13 K' + (0.027 + 0.012 K') cost us at K = 1000 K', that tile's 3.3 + 2.3
-// K' with 8-bit products and 3.4 + 4.3 K' with exact ones: with bf16 output a short K is for the tile
-// (333 x 2304 x 768: 5.7 us against 7.1; at K = 9216 28 against 22.4).
+// K' with 8-bit products and 3.4 + 4.3 K' with exact ones: a costly round at a short K is for the tile (bf16:
+// 333 x 2304 x 768 5.7 us against 7.1, at K = 9216 28 against 22.4; fp32: 2156 x 496 x 128 4.6 against 5.7).
 bool gemm_fp8_narrow_takes(const Fp8Problem &p)
 {
     if (p.M <= kFp8NarrowMaxM)
@@ -327,7 +327,7 @@ bool gemm_fp8_narrow_takes(const Fp8Problem &p)
     if (p.M * p.N > (int64_t)cus * 96 * 48)
         return false;  // more than one round whatever the choice
     const Runs r = pick_runs(p, cus);
-    return r.one_round && (!p.out_bf16 || r.cost <= 64.0 + (double)p.K / 64);
+    return r.one_round && r.cost <= (p.out_bf16 ? 64.0 + (double)p.K / 80 : 100.0 + (double)p.K / 32);
 }
 
 void gemm_fp8_narrow_shape(const Fp8Problem &p, int *rows, int *cols)
