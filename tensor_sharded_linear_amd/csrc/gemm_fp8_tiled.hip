@@ -12,9 +12,9 @@
 //  * mainloop_exact (fp32 output): the codes are widened to bf16 times their scale, which is exact,
 //    and multiplied by v_mfma_f32_16x16x32_bf16 at half the rate.
 //
-// Bound by the matrix cores.  4608 x 9216 x 6144 takes 184 us (2.83 PF; 196 with bias and GELU), where the
+// Bound by the matrix cores.  4608 x 9216 x 6144 takes 184 us (2.83 PF; about 200 with bias and GELU), where the
 // vendor library's e4m3 product with one scale per tensor takes 188; 8192^3 369 us (2.98 PF).  fp32
-// output: 4608 x 6144 x 4608 takes 174 us (1.50 PF; the vendor's bf16 product 169).  The matrix cores are
+// output: 4608 x 6144 x 4608 takes 174 to 182 us (1.50 PF; the vendor's bf16 product 169).  The matrix cores are
 // busy 55 to 65% of a launch's cycles; the rest is the start and the epilogue of each tile (about 8 us of
 // 62), the last round's gap, and loads that land late.
 //
