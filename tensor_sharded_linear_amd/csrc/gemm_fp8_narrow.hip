@@ -259,17 +259,22 @@ hipError_t launch_mb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
 template <int NB, bool GATED>
 hipError_t launch_nb(const NarrowParams &np, bool out_bf16, hipStream_t stream)
 {
-    switch ((np.m_rows + 15) / 16) {
+    const int blocks = (np.m_rows + 15) / 16;
+    switch (blocks) {
     case 1: return launch_mb<1, NB, GATED>(np, out_bf16, stream);
     case 2: return launch_mb<2, NB, GATED>(np, out_bf16, stream);
     case 3: return launch_mb<3, NB, GATED>(np, out_bf16, stream);
-    case 4: return launch_mb<4, NB, GATED>(np, out_bf16, stream);
-    case 5: return launch_mb<5, NB, GATED>(np, out_bf16, stream);
-    default:
+    }
+    // pick_runs gives more than 48 rows at least two blocks of columns, and SwiGLU more than 80 rows two
+    if constexpr (NB > 1) {
+        if (blocks == 4)
+            return launch_mb<4, NB, GATED>(np, out_bf16, stream);
+        if (blocks == 5)
+            return launch_mb<5, NB, GATED>(np, out_bf16, stream);
         if constexpr (NB <= 3)
             return launch_mb<6, NB, GATED>(np, out_bf16, stream);
-        return hipErrorInvalidValue;  // pick_runs gives SwiGLU more than 80 rows at two blocks
     }
+    return hipErrorInvalidValue;
 }
 
 // Output columns and activation rows per workgroup.  Every workgroup streams its weight rows (from
@@ -297,7 +302,8 @@ Runs pick_runs(const Fp8Problem &p, int cus)
         const uint32_t chunks = (M + 16 * blocks - 1) / (16 * blocks), m_rows = (M + chunks - 1) / chunks;
         // MB + NB <= 9 blocks fit the ring: three, or with SwiGLU, which pairs them, four up to 80 rows
         const uint32_t max_cols = p.swiglu ? (m_rows <= 80 ? 32 : 16) : 48;
-        for (uint32_t cols = max_cols; cols >= 4; cols -= 4) {
+        const uint32_t min_cols = p.swiglu || m_rows <= 48 ? 4 : 20;  // many rows by one block of columns never paid
+        for (uint32_t cols = max_cols; cols >= min_cols; cols -= 4) {
             const uint64_t wgs = (uint64_t)((N + cols - 1) / cols) * chunks;
             const uint32_t c16 = (cols + 15) / 16 * 16, m16 = (m_rows + 15) / 16 * 16;
             const double one = (p.swiglu ? 1.0 : 0.5) * (cols + c16) + 0.8 * m16;

@@ -218,6 +218,37 @@ def test_every_tile_with_ragged_edges(m, n, act, out, rows, cols, k):
     assert bool(((y - want).abs() <= bound).all())
 
 
+# A problem for every instance of the split-K kernel: (m, n, act, its row blocks, its blocks of weight rows).
+SPLITS = [(5, 48, "none", 1, 1), (21, 2576, "none", 2, 1), (35, 2736, "none", 3, 1), (1, 4368, "none", 1, 2), (23, 4368, "none", 2, 2),
+          (41, 4368, "none", 3, 2), (51, 6272, "none", 4, 2), (70, 6272, "none", 5, 2), (85, 6272, "none", 6, 2),
+          (9, 8464, "none", 1, 3), (31, 8464, "none", 2, 3), (47, 8464, "none", 3, 3), (63, 8464, "none", 4, 3), (79, 8464, "none", 5, 3),
+          (95, 8464, "none", 6, 3), (2, 144, "swiglu", 1, 2), (27, 2064, "swiglu", 2, 2), (39, 2064, "swiglu", 3, 2),
+          (57, 2576, "swiglu", 4, 2), (67, 2736, "swiglu", 5, 2), (267, 1360, "swiglu", 6, 2), (3, 4368, "swiglu", 1, 4),
+          (25, 4368, "swiglu", 2, 4), (37, 4368, "swiglu", 3, 4), (61, 4368, "swiglu", 4, 4), (78, 4368, "swiglu", 5, 4)]
+
+
+@pytest.mark.parametrize("m,n,act,mb,nb", SPLITS)
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("k", [384, 4736])
+def test_every_split_with_ragged_edges(m, n, act, mb, nb, out, k):
+    """Integer operands, so that sums are exact; the activation's bound is that of ref.linear."""
+    if m > 96:
+        k = 4736  # a tile's at the shorter K
+    rows, cols = tsl.tp_linear_fp8_tile_shape(m, n, k, act, out)
+    assert rows == 16 * mb and -(-cols // 16) * (2 if act == "swiglu" else 1) == nb, (rows, cols)
+    g = torch.Generator().manual_seed(m + n)
+    x, w = _integers(g, m, k), _integers(g, 2 * n if act == "swiglu" else n, k)
+    b = torch.randint(-8, 9, (w[0].shape[0],), generator=g).to(BF).cuda()
+    y = tsl.tp_linear_colwise_fp8(*x, *w, b, act=act, out_dtype=out).double()
+    s = ref.values(*x).cuda() @ ref.values(*w).cuda().t().contiguous() + b.double()
+    if act == "none":
+        assert torch.equal(y, s.to(out).double())
+        return
+    want = s[:, :n] * torch.sigmoid(s[:, :n]) * s[:, n:]
+    bound = 1e-5 * (1 + want.abs()) * 1.01 + ref.HALF_STEP[out] * want.abs()
+    assert bool(((y - want).abs() <= bound).all())
+
+
 @pytest.mark.parametrize("m,n", [(90, 128), (500, 128), (129, 9200), (1000, 4592), (2290, 6128)])
 @pytest.mark.parametrize("out", [BF, F32])
 def test_output_rows_beyond_32_bit_offsets(m, n, out):
